@@ -1,0 +1,96 @@
+// Internal interface between the C ABI of the cache operators (rra_cache_api.cu) and their kernels
+// (rope_append.cu, paged_decode.cu, cache_evict.cu).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "rra_cache.h"
+
+namespace rra {
+
+// Entries that one CTA step of the decode kernel covers (4 warps of 16), and the granule in which
+// its work is split over the grid.
+constexpr int kDecodeUnit = 64;
+// Query heads of a KV head that one warp of the decode kernel carries (the upper half of the 16
+// rows of its MMA tiles holds the low parts of the weights).
+constexpr int kDecodeHeads = 8;
+
+// The cache as the kernels see it.
+struct CacheView {
+  int batch, hq, hkv, g, d;
+  int ps, ps_shift;            // page size, and its logarithm if it is a power of two, else -1
+  int num_pages, max_pages, cap;   // cap = max_pages * ps
+  int64_t page_bytes, head_bytes, entry_bytes;
+  int64_t table_stride;
+  uint8_t *k, *v;
+  const int32_t *table;
+  int32_t *len;
+  float *weight;
+  int32_t *order;
+  int32_t *seen;
+  uint32_t *status;            // sticky error word of the workspace
+};
+
+// Workspace of a cache (byte offsets). Header: the status word, then the append kernel's count of
+// finished blocks. The counters are zero between calls: the block that completes a count resets it.
+struct CacheLayout {
+  size_t status, done, counters;   // counters: int32 per (sequence, KV head, head tile)
+  size_t part_o, part_ml;          // partial outputs and (max, sum) of the decode pieces
+  size_t lse2;                     // fp32 [batch, hq]: log2 of the softmax denominators
+  size_t skip, plan;               // int32 [batch]; int32 [batch * hkv] moves, then [batch] lengths
+  size_t owner;                    // int32 [num_pages]
+  size_t big;                      // logits [batch, hq, cap64], or the evict kernel's move lists
+  size_t total;
+  int grid;                        // CTAs of the decode kernel
+  int head_tiles;                  // ceil(g / kDecodeHeads)
+  int64_t cap64;                   // cap rounded up to kDecodeUnit
+  int64_t moves;                   // places of one move list
+};
+
+CacheLayout cache_layout(const CacheView &c, bool tracked, int num_sms);
+
+struct RopeParams {
+  int batch, hq, hkv, tokens, d, rot;
+  int heads;          // rows of heads per token: hq + hkv (+ hkv with v), those that are given
+  int heads_per_thread;
+  int inverse;
+  rra_positions pos;
+  rra_view q, k, v, qo, ko, vo;   // byte strides
+  const int32_t *new_len;
+  int advance;
+  uint32_t *done;
+  uint64_t turn[RRA_ROPE_MAX_PAIRS];
+  uint8_t axis[RRA_ROPE_MAX_PAIRS];
+};
+
+struct DecodeParams {
+  CacheView c;
+  const uint8_t *q;
+  uint8_t *out;
+  int64_t q_batch, q_head, o_batch, o_head;   // bytes
+  float *lse;
+  float scale_log2;
+  int head_tiles, grid;
+  float *part_o;
+  float2 *part_ml;
+  int32_t *counters;
+  float *lse2;
+  float *logits;      // NULL unless weights are accumulated
+  int64_t cap64;
+};
+
+struct EvictParams {
+  CacheView c;
+  int budget, sinks, recent, advance;
+  int32_t *skip, *plan, *owner;
+  int32_t *moves;
+  int64_t moves_cap;
+};
+
+cudaError_t launch_rope(const RopeParams &p, const CacheView *cache, int dtype, int pairing,
+                        int num_sms, cudaStream_t stream);
+cudaError_t launch_decode(const DecodeParams &p, int dtype, int num_sms, cudaStream_t stream);
+cudaError_t launch_evict(const EvictParams &p, int num_sms, cudaStream_t stream);
+
+}  // namespace rra

@@ -16,6 +16,9 @@ namespace rra {
 // ---------------------------------------------------------------- device status word bits
 constexpr uint32_t kErrTimeout = 1u;   // a bounded barrier wait expired
 constexpr uint32_t kErrBadList = 2u;   // a kept list entry was out of range / not ascending
+constexpr uint32_t kErrBadPage = 4u;   // a page table entry of a cache was out of range
+constexpr uint32_t kErrBadLength = 8u; // a cache length was negative or beyond the page table
+constexpr uint32_t kErrSharedPage = 16u;  // a page to be compacted was in the tables twice
 
 // Default time limit of a barrier wait: a wait that has not completed after this long gives up
 // (sets kErrTimeout and aborts the CTA). The launchers pass the limit in each kernel's

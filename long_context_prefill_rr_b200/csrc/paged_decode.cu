@@ -1,0 +1,440 @@
+// Attention of one new token per sequence over a paged key-value cache, split over the entries
+// and joined: o = sum_e softmax(scale q.k_e) v_e with the running maximum and sum of an online
+// softmax, one pass over K and V.
+//
+// Memory bound: 4 d bytes per entry and KV head against 4 d flop per query head, so K and V have to
+// be read once, at HBM speed, and everything else stays in registers.
+//
+// Work. The entries of all (sequence, KV head, head tile) items are laid end to end in units of 64
+// and cut into equal runs, one per CTA, whatever the lengths are (they are read on the device, so a
+// captured graph follows them). A run touches a few items; its share of one item is a piece. An
+// item of one piece is finished where it is computed; otherwise each piece leaves its unnormalised
+// output, maximum and sum in the workspace and the CTA that finishes last joins them in order of
+// the entries, so equal calls give equal bits.
+//
+// Inner loop. A warp takes 16 entries at a time and shares nothing with the others until its
+// piece ends. Rows go from global memory straight into MMA fragments: the contraction index of
+// q.k may be permuted freely as long as q is permuted alike, so a thread loads 16 bytes of a
+// key row and uses them as the B fragments of two k-steps; the columns of p.v may be permuted as
+// well, so a thread loads 16 bytes of each of four value rows and pairs up the rows' elements. The
+// 8 query heads fill rows 0-7 of the 16-row MMA tile. Rows 8-15 of the p.v product hold the low parts
+// of the same weights (p = hi + lo, both 16-bit), so the weights keep twice the bits of the element
+// type at no cost.
+#include <math.h>
+
+#include "cache_device.cuh"
+
+namespace rra {
+
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+
+// Where a CTA's run of units starts.
+struct Cursor {
+  int b;         // sequence
+  int start;     // first unit of the sequence
+  int units;     // units of one of its items
+  int len;
+};
+
+__device__ __forceinline__ int units_of(int len) { return (len + kDecodeUnit - 1) / kDecodeUnit; }
+
+// Units of all sequences, and the sequence that holds unit `per * cta`. All threads of the block
+// call it; items: items per sequence. Returns the number of units per CTA.
+__device__ int locate(const CacheView &c, int items, int grid, int cta, int *s_scan, Cursor *cur,
+                      int *total_out) {
+  const int tid = threadIdx.x, nt = blockDim.x;
+  const int lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
+  if (c.batch == 1) {
+    const int len = cache_len(c, 0);
+    cur->b = 0;
+    cur->start = 0;
+    cur->units = units_of(len);
+    cur->len = len;
+    *total_out = cur->units * items;
+    return max(1, (*total_out + grid - 1) / grid);
+  }
+  const int chunk = (c.batch + nt - 1) / nt;
+  const int b0 = min(tid * chunk, c.batch), b1 = min(b0 + chunk, c.batch);
+  int sum = 0;
+  for (int b = b0; b < b1; ++b) sum += units_of(cache_len(c, b)) * items;
+  int incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
+  }
+  if (lane == 31) s_scan[warp] = incl;
+  __syncthreads();
+  int before = 0, total = 0;
+  for (int w = 0; w < nw; ++w) {
+    if (w < warp) before += s_scan[w];
+    total += s_scan[w];
+  }
+  const int per = max(1, (total + grid - 1) / grid);
+  const int first = per * cta;
+  int excl = before + incl - sum;
+  if (first >= excl && first < excl + sum) {
+    for (int b = b0; b < b1; ++b) {
+      const int len = cache_len(c, b);
+      const int n = units_of(len) * items;
+      if (first < excl + n) {
+        s_scan[16] = b;
+        s_scan[17] = excl;
+        s_scan[18] = len;
+        break;
+      }
+      excl += n;
+    }
+  }
+  __syncthreads();
+  if (first < total) {
+    cur->b = s_scan[16];
+    cur->start = s_scan[17];
+    cur->len = s_scan[18];
+    cur->units = units_of(cur->len);
+  }
+  *total_out = total;
+  return per;
+}
+
+// The next sequence with entries.
+__device__ __forceinline__ void next_sequence(const CacheView &c, int items, Cursor *cur) {
+  cur->start += cur->units * items;
+  do {
+    ++cur->b;
+    cur->len = cache_len(c, cur->b);
+  } while (cur->len == 0 && cur->b + 1 < c.batch);
+  cur->units = units_of(cur->len);
+}
+
+template <class T, int D>
+__global__ void __launch_bounds__(kThreads, 3)
+    paged_decode_kernel(const __grid_constant__ DecodeParams p) {
+  constexpr int NJ = D / 32;        // 16-byte vectors of a key row per thread
+  constexpr int NH = D / 64;        // 64-dimension halves of a value row
+  constexpr int ROW = D + 4;        // padded row of the merge buffer
+  __shared__ int s_scan[20];
+  __shared__ float s_o[kWarps][kDecodeHeads][ROW];
+  __shared__ float s_m[kWarps][kDecodeHeads], s_l[kWarps][kDecodeHeads];
+
+  const CacheView &c = p.c;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int r = lane >> 2, t = lane & 3;
+  const int items = c.hkv * p.head_tiles;
+  const int cta = blockIdx.x;
+
+  // sequences without entries, and lengths outside the table
+  for (int b = cta; b < c.batch; b += gridDim.x) {
+    const int raw = c.len[b];
+    if ((raw < 0 || raw > c.cap) && threadIdx.x == 0) raise(c.status, kErrBadLength);
+    if (raw > 0) continue;
+    for (int i = threadIdx.x; i < c.hq * (D / 8); i += kThreads) {
+      const int h = i / (D / 8), v = i - h * (D / 8);
+      *reinterpret_cast<uint4 *>(p.out + b * p.o_batch + h * p.o_head + v * 16) =
+          make_uint4(0, 0, 0, 0);
+      if (v == 0) {
+        if (p.lse) p.lse[b * c.hq + h] = -INFINITY;
+        p.lse2[b * c.hq + h] = -INFINITY;
+      }
+    }
+  }
+
+  Cursor cur;
+  int total;
+  const int per = locate(c, items, gridDim.x, cta, s_scan, &cur, &total);
+  int pos = per * cta;
+  const int end = min(pos + per, total);
+
+  while (pos < end) {
+    const int in_seq = pos - cur.start;
+    const int m = in_seq / cur.units;                    // item of the sequence
+    const int unit0 = in_seq - m * cur.units;
+    const int n = min(cur.units - unit0, end - pos);
+    const int head = m / p.head_tiles;                   // KV head
+    const int tile = m - head * p.head_tiles;
+    const int rows = min(kDecodeHeads, c.g - tile * kDecodeHeads);
+    const int h0 = head * c.g + tile * kDecodeHeads;     // first query head
+    const int b = cur.b;
+    const int key1 = min(cur.len, (unit0 + n) * kDecodeUnit);
+
+    uint4 qf[NJ];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+      qf[j] = r < rows ? *reinterpret_cast<const uint4 *>(p.q + b * p.q_batch +
+                                                          (h0 + r) * p.q_head + (4 * j + t) * 16)
+                       : make_uint4(0, 0, 0, 0);
+
+    float acc[NH * 8][4];
+#pragma unroll
+    for (int i = 0; i < NH * 8; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) acc[i][q] = 0.f;
+    float m_run = -INFINITY, l_run = 0.f;
+
+    // byte offset of entry kb + (lane & 15), or -1 if there is none
+    auto place = [&](int kb) -> int64_t {
+      const int e = kb + (lane & 15);
+      if (e >= key1) return -1;
+      int slot, off;
+      split_entry(c, e, slot, off);
+      const int pg = page_at(c, b, slot);
+      return pg < 0 ? -1 : pg * c.page_bytes + off * c.entry_bytes;
+    };
+    const uint8_t *kh = c.k + head * c.head_bytes + t * 16;
+    const uint8_t *vh = c.v + head * c.head_bytes + r * 16;
+
+    int kb = unit0 * kDecodeUnit + warp * 16;
+    int64_t at = place(kb);
+    for (; kb < key1; kb += kDecodeUnit) {
+      int64_t vo[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        vo[i] = __shfl_sync(0xffffffffu, at, 2 * t + (i & 1) + (i >> 1) * 8);
+      uint4 kf[2][NJ], vf[4][NH];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int64_t ko = __shfl_sync(0xffffffffu, at, r + 8 * i);
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+          kf[i][j] = ko >= 0 ? ldg_stream(kh + ko + j * 64) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int h = 0; h < NH; ++h)
+          vf[i][h] = vo[i] >= 0 ? ldg_stream(vh + vo[i] + h * 128) : make_uint4(0, 0, 0, 0);
+      at = place(kb + kDecodeUnit);
+
+      // logits of entries 2t, 2t + 1 (first MMA tile) and 8 + 2t, 8 + 2t + 1 (second), head r
+      float s[2][4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          Elem<T>::mma(s[i], qf[j].x, 0u, qf[j].y, 0u, kf[i][j].x, kf[i][j].y);
+          Elem<T>::mma(s[i], qf[j].z, 0u, qf[j].w, 0u, kf[i][j].z, kf[i][j].w);
+        }
+      }
+      float x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        x[i] = vo[i] >= 0 ? s[i >> 1][i & 1] * p.scale_log2 : -INFINITY;
+      if (p.logits && r < rows) {
+        float *lg = p.logits + (static_cast<int64_t>(b) * c.hq + h0 + r) * p.cap64 + kb + 2 * t;
+        if (kb + 2 * t < key1) *reinterpret_cast<float2 *>(lg) = make_float2(x[0], x[1]);
+        if (kb + 8 + 2 * t < key1) *reinterpret_cast<float2 *>(lg + 8) = make_float2(x[2], x[3]);
+      }
+      float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      if (__any_sync(0xffffffffu, mx > m_run)) {
+        const float m_new = fmaxf(m_run, mx);
+        // a row that has met no logit yet stays at -inf with sums of zero
+        const float alpha = m_new == -INFINITY ? 1.f : exp2f(m_run - m_new);
+        m_run = m_new;
+        l_run *= alpha;
+#pragma unroll
+        for (int i = 0; i < NH * 8; ++i)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) acc[i][q] *= alpha;
+      }
+      const float base = m_run == -INFINITY ? 0.f : m_run;
+      float w[4], lo[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        w[i] = exp2f(x[i] - base);
+        l_run += w[i];
+      }
+      const uint32_t hi0 = Elem<T>::pack(w[0], w[1]), hi1 = Elem<T>::pack(w[2], w[3]);
+      const float2 f0 = Elem<T>::unpack(hi0), f1 = Elem<T>::unpack(hi1);
+      lo[0] = w[0] - f0.x;
+      lo[1] = w[1] - f0.y;
+      lo[2] = w[2] - f1.x;
+      lo[3] = w[3] - f1.y;
+      const uint32_t lo0 = Elem<T>::pack(lo[0], lo[1]), lo1 = Elem<T>::pack(lo[2], lo[3]);
+#pragma unroll
+      for (int h = 0; h < NH; ++h) {
+        const uint32_t *v0 = reinterpret_cast<const uint32_t *>(&vf[0][h]);
+        const uint32_t *v1 = reinterpret_cast<const uint32_t *>(&vf[1][h]);
+        const uint32_t *v2 = reinterpret_cast<const uint32_t *>(&vf[2][h]);
+        const uint32_t *v3 = reinterpret_cast<const uint32_t *>(&vf[3][h]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t pick = (e & 1) ? 0x7632u : 0x5410u;
+          Elem<T>::mma(acc[h * 8 + e], hi0, lo0, hi1, lo1,
+                       __byte_perm(v0[e >> 1], v1[e >> 1], pick),
+                       __byte_perm(v2[e >> 1], v3[e >> 1], pick));
+        }
+      }
+    }
+
+    // ---- the warps' results meet in shared memory
+    l_run += __shfl_xor_sync(0xffffffffu, l_run, 1);
+    l_run += __shfl_xor_sync(0xffffffffu, l_run, 2);
+    if (t == 0) {
+      s_m[warp][r] = m_run;
+      s_l[warp][r] = l_run;
+    }
+    // the thread's columns 2t and 2t + 1 of the permuted tiles are dimensions 16t .. 16t + 15 of
+    // each half; high and low parts of the weights are added here
+#pragma unroll
+    for (int h = 0; h < NH; ++h)
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int e = 0; e < 8; e += 4)
+          *reinterpret_cast<float4 *>(&s_o[warp][r][h * 64 + t * 16 + q * 8 + e]) =
+              make_float4(acc[h * 8 + e][q] + acc[h * 8 + e][q + 2],
+                          acc[h * 8 + e + 1][q] + acc[h * 8 + e + 1][q + 2],
+                          acc[h * 8 + e + 2][q] + acc[h * 8 + e + 2][q + 2],
+                          acc[h * 8 + e + 3][q] + acc[h * 8 + e + 3][q + 2]);
+    __syncthreads();
+
+    const int first_unit = cur.start + m * cur.units;
+    const int cta0 = first_unit / per, cta1 = (first_unit + cur.units - 1) / per;
+    const int item = b * items + m;
+    const int64_t slot = static_cast<int64_t>(cta) + item;
+    const bool whole = cta0 == cta1;
+    for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads) {
+      const int row = i / (D / 4), col = (i - row * (D / 4)) * 4;
+      float mt = s_m[0][row];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) mt = fmaxf(mt, s_m[w][row]);
+      const float base = mt == -INFINITY ? 0.f : mt;
+      float l = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = exp2f(s_m[w][row] - base);
+        const float4 x = *reinterpret_cast<const float4 *>(&s_o[w][row][col]);
+        l += f * s_l[w][row];
+        o.x += f * x.x;
+        o.y += f * x.y;
+        o.z += f * x.z;
+        o.w += f * x.w;
+      }
+      if (whole) {
+        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);   // NaN stays
+        *reinterpret_cast<uint2 *>(p.out + b * p.o_batch + (h0 + row) * p.o_head + col * 2) =
+            make_uint2(Elem<T>::pack(o.x * inv, o.y * inv), Elem<T>::pack(o.z * inv, o.w * inv));
+        if (col == 0) {
+          const float l2 = base + log2f(l);
+          p.lse2[b * c.hq + h0 + row] = l2;
+          if (p.lse) p.lse[b * c.hq + h0 + row] = l2 * 0.6931471805599453f;
+        }
+      } else {
+        *reinterpret_cast<float4 *>(p.part_o + (slot * kDecodeHeads + row) * D + col) = o;
+        if (col == 0) p.part_ml[slot * kDecodeHeads + row] = make_float2(mt, l);
+      }
+    }
+
+    if (!whole) {
+      // ---- the last of the item's CTAs joins its pieces, in the order of the entries
+      __threadfence();
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        const int done = atomicAdd(&p.counters[item], 1);
+        s_scan[19] = done == cta1 - cta0;
+        if (done == cta1 - cta0) p.counters[item] = 0;
+      }
+      __syncthreads();
+      if (s_scan[19]) {
+        __threadfence();
+        for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads) {
+          const int row = i / (D / 4), col = (i - row * (D / 4)) * 4;
+          float mt = -INFINITY, l = 0.f;
+          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+          const float2 *ml = p.part_ml + (static_cast<int64_t>(item) + cta0) * kDecodeHeads + row;
+          const float *po =
+              p.part_o + ((static_cast<int64_t>(item) + cta0) * kDecodeHeads + row) * D + col;
+          for (int k = cta0; k <= cta1; ++k, ml += kDecodeHeads, po += kDecodeHeads * D) {
+            const float2 y = __ldcg(ml);
+            const float4 x = __ldcg(reinterpret_cast<const float4 *>(po));
+            const float mn = fmaxf(mt, y.x);
+            const float base = mn == -INFINITY ? 0.f : mn;
+            const float fa = exp2f(mt - base), fb = exp2f(y.x - base);
+            mt = mn;
+            l = l * fa + y.y * fb;
+            o.x = o.x * fa + x.x * fb;
+            o.y = o.y * fa + x.y * fb;
+            o.z = o.z * fa + x.z * fb;
+            o.w = o.w * fa + x.w * fb;
+          }
+          const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+          *reinterpret_cast<uint2 *>(p.out + b * p.o_batch + (h0 + row) * p.o_head + col * 2) =
+              make_uint2(Elem<T>::pack(o.x * inv, o.y * inv),
+                         Elem<T>::pack(o.z * inv, o.w * inv));
+          if (col == 0) {
+            const float l2 = (mt == -INFINITY ? 0.f : mt) + log2f(l);
+            p.lse2[b * c.hq + h0 + row] = l2;
+            if (p.lse) p.lse[b * c.hq + h0 + row] = l2 * 0.6931471805599453f;
+          }
+        }
+      }
+    }
+    __syncthreads();   // the merge buffer is free again
+    pos += n;
+    if (pos < end && pos - cur.start == cur.units * items) next_sequence(c, items, &cur);
+  }
+}
+
+// weight[entry, KV head] += sum over the KV head's query heads of 2^(logit - lse2). One thread per
+// entry; the logits of the pass before are read once, most of them from L2.
+__global__ void __launch_bounds__(kThreads) add_weight_kernel(const __grid_constant__ DecodeParams p) {
+  __shared__ int s_scan[20];
+  const CacheView &c = p.c;
+  Cursor cur;
+  int total;
+  const int per = locate(c, c.hkv, gridDim.x, blockIdx.x, s_scan, &cur, &total);
+  int pos = per * blockIdx.x;
+  const int end = min(pos + per, total);
+  while (pos < end) {
+    const int in_seq = pos - cur.start;
+    const int head = in_seq / cur.units;
+    const int unit0 = in_seq - head * cur.units;
+    const int n = min(cur.units - unit0, end - pos);
+    const int key1 = min(cur.len, (unit0 + n) * kDecodeUnit);
+    const int64_t row0 = static_cast<int64_t>(cur.b) * c.hq + head * c.g;
+    for (int e = unit0 * kDecodeUnit + threadIdx.x; e < key1; e += kThreads) {
+      int slot, off;
+      split_entry(c, e, slot, off);
+      const int pg = page_at(c, cur.b, slot);
+      if (pg < 0) continue;
+      float sum = 0.f;
+      for (int h = 0; h < c.g; ++h) {
+        const float l2 = p.lse2[row0 + h];
+        const float x = p.logits[(row0 + h) * p.cap64 + e];
+        // a row whose every logit is -inf has no weights
+        sum += l2 == -INFINITY ? 0.f : exp2f(x - l2);
+      }
+      atomicAdd(c.weight + track_at(c, pg, head, off), sum);
+    }
+    pos += n;
+    if (pos < end && pos - cur.start == cur.units * c.hkv) next_sequence(c, c.hkv, &cur);
+  }
+}
+
+template <class T>
+cudaError_t launch_decode_t(const DecodeParams &p, cudaStream_t stream) {
+  if (p.c.d == 128)
+    paged_decode_kernel<T, 128><<<p.grid, kThreads, 0, stream>>>(p);
+  else
+    paged_decode_kernel<T, 64><<<p.grid, kThreads, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_decode(const DecodeParams &p, int dtype, int num_sms, cudaStream_t stream) {
+  cudaError_t e = dtype == RRA_BF16 ? launch_decode_t<__nv_bfloat16>(p, stream)
+                                    : launch_decode_t<__half>(p, stream);
+  if (e != cudaSuccess || !p.logits) return e;
+  add_weight_kernel<<<num_sms * 8, kThreads, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace rra

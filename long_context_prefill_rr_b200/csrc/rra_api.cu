@@ -407,7 +407,7 @@ rra_status rra_check_device_status(void *workspace, rra_stream_t stream, uint32_
     if (cudaStreamSynchronize(st) != cudaSuccess) return RRA_ERR_CUDA;
   }
   if (word & rra::kErrTimeout) return RRA_ERR_DEVICE_TIMEOUT;
-  if (word & rra::kErrBadList) return RRA_ERR_INVALID_ARG;
+  if (word != 0) return RRA_ERR_INVALID_ARG;   // a bad kept list, page table or cache length
   return RRA_OK;
 }
 

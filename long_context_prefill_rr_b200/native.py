@@ -19,7 +19,7 @@ STATUS_NAMES = {
     4: "RRA_ERR_CUDA", 5: "RRA_ERR_DEVICE_TIMEOUT",
 }
 
-# every entry point declared in include/rra.h, with its ctypes signature
+# every entry point declared in include/rra.h and include/rra_cache.h, with its ctypes signature
 _c = ctypes
 _SIGS = {
     "rra_workspace_bytes": (_c.c_size_t, [_c.c_void_p]),
@@ -47,6 +47,16 @@ _SIGS = {
     "rra_set_wait_limit_ns": (None, [_c.c_uint64]),
     "rra_status_string": (_c.c_char_p, [_c.c_int]),
     "rra_version": (_c.c_char_p, []),
+    "rra_rope_init": (_c.c_int, [_c.c_void_p, _c.c_int, _c.c_int, _c.c_int, _c.c_int, _c.c_double,
+                                 _c.c_void_p, _c.c_void_p, _c.c_void_p]),
+    "rra_rope_rotate": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_int, _c.c_void_p]),
+    "rra_cache_workspace_bytes": (_c.c_size_t, [_c.c_void_p]),
+    "rra_cache_append": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_int,
+                                    _c.c_void_p]),
+    "rra_cache_decode": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_int,
+                                    _c.c_void_p]),
+    "rra_cache_evict": (_c.c_int, [_c.c_void_p, _c.c_int, _c.c_int, _c.c_int, _c.c_int,
+                                   _c.c_void_p]),
 }
 
 
