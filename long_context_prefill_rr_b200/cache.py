@@ -14,6 +14,9 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import struct
+
+import torch
 
 from . import native
 
@@ -62,15 +65,15 @@ class _Cache(_c.Structure):
 
 
 def _dtype_code(t, name):
-    import torch
-    if t.dtype == torch.bfloat16:
-        return 0
-    if t.dtype == torch.float16:
-        return 1
-    raise ValueError(f"{name} must be bfloat16 or float16, got {t.dtype}")
+    code = _CODES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be bfloat16 or float16, got {t.dtype}")
+    return code
 
 
 def _need(t, name, device, dtype, shape):
+    if t.dtype is dtype and t.shape == shape and t.device == device:
+        return
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, is on {t.device}")
     if t.dtype != dtype:
@@ -90,16 +93,17 @@ def _cuda(t, name):
     return t.device
 
 
+# A call's views and tokens are packed in one step (field by field costs more than the launch); the
+# classes above give the layout.
+_pack_view = struct.Struct("@P3q").pack
+_pack_tokens = struct.Struct("@5i4x" + "P3q" * 7).pack
+_NO_VIEW = (0, 0, 0, 0)
+_CODES = {torch.bfloat16: 0, torch.float16: 1}
+
+
 def _view4(t):
     s = t.stride()
-    return _View(t.data_ptr(), s[0], s[1], s[2])
-
-
-@contextlib.contextmanager
-def _other_device(device):
-    import torch
-    with torch.cuda.device(device):
-        yield
+    return t.data_ptr(), s[0], s[1], s[2]
 
 
 _here = contextlib.nullcontext()
@@ -107,14 +111,20 @@ _here = contextlib.nullcontext()
 
 def _on(device):
     """Makes the tensors' device current for a call (the library runs on the current one)."""
-    import torch
-    return _here if torch.cuda.current_device() == device.index else _other_device(device)
+    return _here if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+def _current_stream(device):
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+# the same without building a Stream object, where torch has it
+_raw_current = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _raw_stream(stream, device):
-    import torch
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
+        return _raw_current(device.index) if _raw_current else _current_stream(device)
     if stream.device != device:
         raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
     return stream.cuda_stream
@@ -165,51 +175,50 @@ class RopeTable:
 
 
 def _fill_tokens(table, positions, q, k, v, q_out, k_out, v_out):
-    """Checks the tensors of a call and packs them; returns (tokens, device, outputs)."""
-    import torch
+    """Checks the tensors of a call and packs them; returns (tokens, device, heads_q, outputs)."""
     first = k if k is not None else (q if q is not None else v)
     if first is None:
         raise ValueError("nothing to rotate: give q, k or both")
     if first.dim() != 4:
         raise ValueError("q, k and v must have 4 dimensions: [batch, heads, tokens, head_dim]")
-    device, dtype = _cuda(first, "q, k or v"), first.dtype
+    device, dtype = first.device, first.dtype
+    if device.type != "cuda":
+        raise ValueError("q, k and v must be CUDA tensors")
+    code = _dtype_code(first, "q, k and v")
     b, _, n, d = first.shape
     if d != table.head_dim:
         raise ValueError(f"head_dim is {d}, the table's is {table.head_dim}")
-    t = _Tokens()
-    t.batch, t.tokens, t.dtype = b, n, _dtype_code(first, "q, k and v")
-    if positions.device != device or positions.dtype != torch.int32 or \
-            positions.shape != (table.axes, b, n):
-        raise ValueError(f"positions must be int32 {(table.axes, b, n)} on {device}, got "
-                         f"{positions.dtype} {tuple(positions.shape)} on {positions.device}")
-    s = positions.stride()
-    t.positions = _Positions(positions.data_ptr(), s[0], s[1], s[2])
-    outs = []
+    _need(positions, "positions", device, torch.int32, (table.axes, b, n))
+    heads = {"q": 0, "k": 0, "v": 0}
+    views, outs = [], []
     for name, x, o in (("q", q, q_out), ("k", k, k_out), ("v", v, v_out)):
         if x is None:
             if o is not None:
                 raise ValueError(f"{name}_out is given without {name}")
+            views.append(_NO_VIEW)
             outs.append(None)
             continue
-        heads = x.shape[1] if x.dim() == 4 else -1
-        if x is not first:
-            _need(x, name, device, dtype, (b, heads, n, d))
+        shape = x.shape
+        if len(shape) != 4 or shape[0] != b or shape[2] != n or shape[3] != d or \
+                x.dtype is not dtype or x.device != device:
+            raise ValueError(f"{name} must be {dtype} [{b}, heads, {n}, {d}] on {device}, got "
+                             f"{x.dtype} {tuple(shape)} on {x.device}")
         _rows(x, name)
-        if name == "q":
-            t.heads_q = heads
-        elif t.heads_kv and t.heads_kv != heads:
-            raise ValueError(f"k has {t.heads_kv} heads, v has {heads}")
-        else:
-            t.heads_kv = heads
-        setattr(t, name, _view4(x))
+        heads[name] = shape[1]
+        views.append(_view4(x))
         if o is True:
-            o = torch.empty((b, heads, n, d), dtype=dtype, device=device)
-        if o is not None:
-            _need(o, name + "_out", device, dtype, (b, heads, n, d))
+            o = torch.empty(shape, dtype=dtype, device=device)
+        elif o is not None:
+            _need(o, name + "_out", device, dtype, shape)
             _rows(o, name + "_out")
-            setattr(t, name + "_out", _view4(o))
         outs.append(o)
-    return t, device, outs
+    if k is not None and v is not None and heads["k"] != heads["v"]:
+        raise ValueError(f"k has {heads['k']} heads, v has {heads['v']}")
+    out_views = [_NO_VIEW if o is None else _view4(o) for o in outs]
+    t = _pack_tokens(b, heads["q"], heads["k"] or heads["v"], n, code, *_view4(positions),
+                     *views[0], *views[1], *views[2], *out_views[0], *out_views[1],
+                     *out_views[2])
+    return t, device, heads["q"], outs
 
 
 def rope(table, positions, q=None, k=None, v=None, *, q_out=None, k_out=None, v_out=None,
@@ -222,11 +231,11 @@ def rope(table, positions, q=None, k=None, v=None, *, q_out=None, k_out=None, v_
     q_out = True if q is not None and q_out is None else q_out
     k_out = True if k is not None and k_out is None else k_out
     v_out = True if v is not None and v_out is None else v_out
-    t, device, outs = _fill_tokens(table, positions, q, k, v, q_out, k_out, v_out)
+    t, device, _, outs = _fill_tokens(table, positions, q, k, v, q_out, k_out, v_out)
     raw = _raw_stream(stream, device)
     with _on(device):
-        native._check(native.load().rra_rope_rotate(table._ref, _c.byref(t), 1 if inverse else 0,
-                                                    raw), "rra_rope_rotate")
+        status = native.load().rra_rope_rotate(table._ref, t, 1 if inverse else 0, raw)
+    native._check(status, "rra_rope_rotate")
     outs = [o for o in outs if o is not None]
     return outs[0] if len(outs) == 1 else tuple(outs)
 
@@ -249,7 +258,6 @@ class PagedCache:
 
     def __init__(self, k, v, page_table, lengths, *, heads_q, softmax_scale=-1.0, weight=None,
                  order=None, seen=None):
-        import torch
         device = _cuda(k, "k")
         if k.dim() != 4 or page_table.dim() != 2:
             raise ValueError("k must be [num_pages, heads_kv, page_size, head_dim] and page_table "
@@ -286,8 +294,9 @@ class PagedCache:
                           ptr(page_table), ptr(lengths), ptr(weight), ptr(order), ptr(seen),
                           None, 0)
         self._ref = _c.byref(self.raw)
+        self._lib = native.load()
         with _on(device):
-            n = int(native.load().rra_cache_workspace_bytes(self._ref))
+            n = int(self._lib.rra_cache_workspace_bytes(self._ref))
             if n == 0:
                 raise native.RraError(1, "rra_cache_workspace_bytes")
             self.ws = torch.zeros(n, dtype=torch.uint8, device=device)
@@ -298,7 +307,6 @@ class PagedCache:
     def allocate(cls, batch, max_len, heads_q, heads_kv, head_dim, *, page_size=64, dtype=None,
                  softmax_scale=-1.0, track=False, device="cuda"):
         """An empty cache with pages of its own for ``max_len`` entries per sequence."""
-        import torch
         dtype = torch.bfloat16 if dtype is None else dtype
         per = max(1, -(-max_len // page_size))
         kv = torch.zeros(2, max(1, batch * per), heads_kv, page_size, head_dim, dtype=dtype,
@@ -321,24 +329,24 @@ class PagedCache:
         rest is padding, neither read nor written. ``advance=False`` leaves lengths and seen as they
         are (for all but the last of the layers that share them). Returns q_out, or
         (q_out, k_out, v_out) if k_out or v_out is given."""
-        import torch
         q_out = True if q is not None and q_out is None else q_out
-        t, device, outs = _fill_tokens(table, positions, q, k, v, q_out, k_out, v_out)
-        if v is None:
-            raise ValueError("v is required")
+        if k is None or v is None:
+            raise ValueError("k and v are required")
+        t, device, heads_q, outs = _fill_tokens(table, positions, q, k, v, q_out, k_out, v_out)
         if device != self.device:
             raise ValueError(f"the cache is on {self.device}, the tokens are on {device}")
-        if q is not None and t.heads_q != self.heads_q:
-            raise ValueError(f"q has {t.heads_q} heads, the cache was made for {self.heads_q}")
+        if q is not None and heads_q != self.heads_q:
+            raise ValueError(f"q has {heads_q} heads, the cache was made for {self.heads_q}")
         if new_len is not None:
             _need(new_len, "new_len", device, torch.int32, (self.batch,))
             if not new_len.is_contiguous():
                 raise ValueError("new_len must be contiguous")
         raw = _raw_stream(stream, device)
         with _on(device):
-            native._check(native.load().rra_cache_append(
-                self._ref, table._ref, _c.byref(t), None if new_len is None else
-                new_len.data_ptr(), 1 if advance else 0, raw), "rra_cache_append")
+            status = self._lib.rra_cache_append(
+                self._ref, table._ref, t, None if new_len is None else new_len.data_ptr(),
+                1 if advance else 0, raw)
+        native._check(status, "rra_cache_append")
         return outs[0] if k_out is None and v_out is None else tuple(outs)
 
     def decode(self, q, *, out=None, lse=None, add_weight=False, stream=None):
@@ -346,7 +354,6 @@ class PagedCache:
         [batch, heads_q, 1, head_dim], over the sequence's entries; returns ``out``, like q. ``lse``:
         fp32 [batch, heads_q], receives the logarithm of the softmax's denominator.
         ``add_weight=True`` adds the softmax weights to ``weight``."""
-        import torch
         shape = self._q_shape if q.dim() != 4 else self._q_shape[:2] + (1, self._q_shape[2])
         _need(q, "q", self.device, self.k.dtype, shape)
         _rows(q, "q")
@@ -364,11 +371,11 @@ class PagedCache:
         sq, so = q.stride(), out.stride()
         raw = _raw_stream(stream, self.device)
         with _on(self.device):
-            native._check(native.load().rra_cache_decode(
-                self._ref, _c.byref(_View(q.data_ptr(), sq[0], sq[1], 0)),
-                _c.byref(_View(out.data_ptr(), so[0], so[1], 0)),
-                None if lse is None else lse.data_ptr(), 1 if add_weight else 0, raw),
-                "rra_cache_decode")
+            status = self._lib.rra_cache_decode(
+                self._ref, _pack_view(q.data_ptr(), sq[0], sq[1], 0),
+                _pack_view(out.data_ptr(), so[0], so[1], 0),
+                None if lse is None else lse.data_ptr(), 1 if add_weight else 0, raw)
+        native._check(status, "rra_cache_decode")
         return out
 
     def evict(self, budget, *, sinks=0, recent=0, advance=True, stream=None):
@@ -380,14 +387,14 @@ class PagedCache:
             raise ValueError("budget, sinks and recent must fit 31 bits and not be negative")
         raw = _raw_stream(stream, self.device)
         with _on(self.device):
-            native._check(native.load().rra_cache_evict(self._ref, budget, sinks, recent,
-                                                        1 if advance else 0, raw),
-                          "rra_cache_evict")
+            status = self._lib.rra_cache_evict(self._ref, budget, sinks, recent,
+                                               1 if advance else 0, raw)
+        native._check(status, "rra_cache_evict")
 
     def check(self, stream=None):
         """Synchronises and raises if a call met a bad page, length or shared page since the last
         check (the error word is cleared)."""
         raw, word = _raw_stream(stream, self.device), _c.c_uint32(0)
         with _on(self.device):
-            st = native.load().rra_check_device_status(self.ws.data_ptr(), raw, _c.byref(word))
+            st = self._lib.rra_check_device_status(self.ws.data_ptr(), raw, _c.byref(word))
         native._check(int(st), f"device status word {word.value:#x}")

@@ -9,6 +9,16 @@
 
 namespace rra {
 
+// Waits until the kernels before this one on the stream are complete and their writes visible; every
+// thread calls it before it touches global memory.
+__device__ __forceinline__ void grid_dependency_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+// Lets the next kernel's blocks be set up from now on (it waits for this grid's end all the same).
+__device__ __forceinline__ void grid_dependents_go() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 __device__ __forceinline__ void raise(uint32_t *status, uint32_t bit) { atomicOr(status, bit); }
 
 // Length of sequence b, clamped to what the page table can hold.
@@ -29,7 +39,7 @@ __device__ __forceinline__ void split_entry(const CacheView &c, int e, int &slot
 
 // Page of table place `slot` of sequence b, or -1 (flagged) if it is not a page of the cache.
 __device__ __forceinline__ int page_at(const CacheView &c, int b, int slot) {
-  const int pg = __ldg(c.table + b * c.table_stride + slot);
+  const int pg = c.table[b * c.table_stride + slot];
   if (static_cast<unsigned>(pg) < static_cast<unsigned>(c.num_pages)) return pg;
   raise(c.status, kErrBadPage);
   return -1;
@@ -40,11 +50,14 @@ __device__ __forceinline__ int64_t track_at(const CacheView &c, int page, int he
   return (static_cast<int64_t>(page) * c.hkv + head) * c.ps + off;
 }
 
-__device__ __forceinline__ uint4 ldg_stream(const void *p) {
+// A row that is read once. (None of these kernels reads through the non-coherent path: they may be set
+// up while the kernel that writes what they read still runs.)
+__device__ __forceinline__ uint4 ld_stream(const void *p) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
+               : "l"(p)
+               : "memory");
   return v;
 }
 

@@ -16,6 +16,9 @@ constexpr int kDecodeUnit = 64;
 // rows of its MMA tiles holds the low parts of the weights).
 constexpr int kDecodeHeads = 8;
 
+// CTAs of the decode kernel that share an SM.
+constexpr int decode_ctas(int head_dim) { return head_dim == 128 ? 2 : 3; }
+
 // The cache as the kernels see it.
 struct CacheView {
   int batch, hq, hkv, g, d;
@@ -32,14 +35,15 @@ struct CacheView {
   uint32_t *status;            // sticky error word of the workspace
 };
 
-// Workspace of a cache (byte offsets). Header: the status word, then the append kernel's count of
-// finished blocks. The counters are zero between calls: the block that completes a count resets it.
+// Workspace of a cache (byte offsets). Header: the status word, the append kernel's count of
+// finished blocks and the eviction's call count. The counters are zero between calls: the block that
+// completes a count resets it.
 struct CacheLayout {
-  size_t status, done, counters;   // counters: int32 per (sequence, KV head, head tile)
+  size_t status, done, epoch, counters;   // counters: int32 per (sequence, KV head, head tile)
   size_t part_o, part_ml;          // partial outputs and (max, sum) of the decode pieces
   size_t lse2;                     // fp32 [batch, hq]: log2 of the softmax denominators
-  size_t skip, plan;               // int32 [batch]; int32 [batch * hkv] moves, then [batch] lengths
-  size_t owner;                    // int32 [num_pages]
+  size_t skip, tags, lens, plan;   // 32-bit [batch], [batch], [batch] and [batch * hkv]
+  size_t owner;                    // uint64 [num_pages]
   size_t big;                      // logits [batch, hq, cap64], or the evict kernel's move lists
   size_t total;
   int grid;                        // CTAs of the decode kernel
@@ -83,10 +87,35 @@ struct DecodeParams {
 struct EvictParams {
   CacheView c;
   int budget, sinks, recent, advance;
-  int32_t *skip, *plan, *owner;
+  uint32_t *epoch;             // calls so far; a call marks what it finds with epoch + 1
+  uint32_t *skip, *tags;       // [batch]: the call that left the sequence alone; the current one
+  int32_t *lens, *plan;        // [batch] lengths; [batch * hkv] moves
+  unsigned long long *owner;   // [num_pages]: tag << 32 | sequence of the last claim
   int32_t *moves;
   int64_t moves_cap;
 };
+
+// Launches a kernel that begins with griddepcontrol.wait: its blocks may be set up while the kernel before
+// it on the stream drains. cluster: blocks per cluster.
+template <class... Params, class... Args>
+cudaError_t launch_dependent(void (*kern)(Params...), dim3 grid, int threads, size_t smem,
+                             int cluster, cudaStream_t stream, const Args &...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
 
 cudaError_t launch_rope(const RopeParams &p, const CacheView *cache, int dtype, int pairing,
                         int num_sms, cudaStream_t stream);

@@ -12,15 +12,25 @@
 // output, maximum and sum in the workspace and the CTA that finishes last joins them in order of
 // the entries, so equal calls give equal bits.
 //
-// Inner loop. A warp takes 16 entries at a time and shares nothing with the others until its
-// piece ends. Rows go from global memory straight into MMA fragments: the contraction index of
-// q.k may be permuted freely as long as q is permuted alike, so a thread loads 16 bytes of a
-// key row and uses them as the B fragments of two k-steps; the columns of p.v may be permuted as
-// well, so a thread loads 16 bytes of each of four value rows and pairs up the rows' elements. The
-// 8 query heads fill rows 0-7 of the 16-row MMA tile. Rows 8-15 of the p.v product hold the low parts
-// of the same weights (p = hi + lo, both 16-bit), so the weights keep twice the bits of the element
-// type at no cost.
+// Inner loop. A warp takes 16 entries at a time through a ring of its own, filled by cp.async, and
+// shares nothing with the other warps until its piece ends: no block barrier in the loop. The MMA
+// fragments come out of the ring by 16-byte reads: the contraction index of q.k may be permuted freely
+// as long as q is permuted alike, so a thread takes 16 bytes of a key row as the B fragments of two
+// k-steps; the columns of p.v may be permuted as well, so a thread takes 16 bytes of each of four
+// value rows and pairs up the rows' elements. The 8 query heads fill rows 0-7 of the 16-row MMA
+// tile. Rows 8-15 of the p.v product hold the low parts of the same weights (p = hi + lo, both 16-bit),
+// so the weights keep twice the bits of the element type at no cost.
+//
+// Measured on the way (128K entries, 32 / 8 heads of 128, 537 MB; the copy rate gives 82 us): fragments
+// loaded straight into registers 107 us (64-byte requests, 56% of the load pipe's wavefronts); the
+// same loads through cp.async into places private to each thread 136; a ring of rows filled by one bulk
+// copy per row 106 (a warp issues its 32 copies one by one); this ring, whose copies cover whole rows,
+// 94. Two stages and two CTAs per SM (three for head_dim 64) keep 128 KB in flight; more bytes in flight
+// are slower (three stages 97, three CTAs 101; head_dim 64 with four stages and three CTAs 106
+// against 88).
 #include <math.h>
+
+#include <atomic>
 
 #include "cache_device.cuh"
 
@@ -30,6 +40,40 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
+
+// A warp's ring: kStages stages of 16 key rows and 16 value rows. Rows lie D * 2 + 32 bytes apart, 8
+// banks past a multiple of 32, which with the order of the entries below keeps every 16-byte read
+// of a warp free of bank conflicts.
+constexpr int kStages = 2;
+template <int D>
+constexpr uint32_t kPitch = D * 2 + 32;
+template <int D>
+constexpr uint32_t kStageBytes = 32 * kPitch<D>;
+template <int D>
+constexpr size_t kRingBytes = static_cast<size_t>(kWarps) * kStages * kStageBytes<D>;
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool valid) {
+  const int n = valid ? 16 : 0;   // 0: nothing is read, the place is filled with zeros
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+// Entry (of 8) behind column 2 t + e of an MMA tile. Columns may stand for the entries in any order, as
+// long as logits, weights and value rows agree; this one puts the rows that a read touches together
+// (columns 2 t, 2 t + 1 of the keys; the four values of t for the value rows) into different banks.
+__device__ __forceinline__ int entry_of(int t, int e) { return e ? 4 + ((t + 2) & 3) : t; }
 
 // Where a CTA's run of units starts.
 struct Cursor {
@@ -111,13 +155,16 @@ __device__ __forceinline__ void next_sequence(const CacheView &c, int items, Cur
 }
 
 template <class T, int D>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, decode_ctas(D))
     paged_decode_kernel(const __grid_constant__ DecodeParams p) {
   constexpr int NJ = D / 32;        // 16-byte vectors of a key row per thread
   constexpr int NH = D / 64;        // 64-dimension halves of a value row
+  constexpr int S = kStages;
+  constexpr uint32_t PITCH = kPitch<D>, STAGE = kStageBytes<D>;
   constexpr int ROW = D + 4;        // padded row of the merge buffer
+  static_assert(S <= 4 && S * STAGE >= kDecodeHeads * ROW * 4, "exist masks, merge buffer");
+  extern __shared__ __align__(128) uint8_t s_ring[];
   __shared__ int s_scan[20];
-  __shared__ float s_o[kWarps][kDecodeHeads][ROW];
   __shared__ float s_m[kWarps][kDecodeHeads], s_l[kWarps][kDecodeHeads];
 
   const CacheView &c = p.c;
@@ -125,7 +172,12 @@ __global__ void __launch_bounds__(kThreads, 3)
   const int r = lane >> 2, t = lane & 3;
   const int items = c.hkv * p.head_tiles;
   const int cta = blockIdx.x;
+  const uint32_t ring = smem_u32(s_ring) + warp * S * STAGE;
+  // the merge buffer of a warp lies over its ring, which is idle then
+  auto s_o = [&](int w) { return reinterpret_cast<float *>(s_ring + w * S * STAGE); };
 
+  grid_dependency_wait();
+  grid_dependents_go();
   // sequences without entries, and lengths outside the table
   for (int b = cta; b < c.batch; b += gridDim.x) {
     const int raw = c.len[b];
@@ -183,50 +235,61 @@ __global__ void __launch_bounds__(kThreads, 3)
       const int pg = page_at(c, b, slot);
       return pg < 0 ? -1 : pg * c.page_bytes + off * c.entry_bytes;
     };
-    const uint8_t *kh = c.k + head * c.head_bytes + t * 16;
-    const uint8_t *vh = c.v + head * c.head_bytes + r * 16;
+    // Starts the copies of 16 entries into a stage: LANES lanes to a row, so that a warp's copy reads whole
+    // rows. Entries that do not exist become rows of zeros. Returns which do.
+    constexpr int LANES = D / 8, ROWS = 32 / LANES;
+    const uint8_t *kh = c.k + head * c.head_bytes + (lane % LANES) * 16;
+    const uint8_t *vh = c.v + head * c.head_bytes + (lane % LANES) * 16;
+    auto fetch = [&](int st, int64_t at) -> uint32_t {
+      const uint32_t dst = ring + st * STAGE + (lane / LANES) * PITCH + (lane % LANES) * 16;
+#pragma unroll
+      for (int i = 0; i < 16 / ROWS; ++i) {
+        const int64_t o = __shfl_sync(0xffffffffu, at, i * ROWS + lane / LANES);
+        const int64_t from = o >= 0 ? o : 0;
+        copy16(dst + i * ROWS * PITCH, kh + from, o >= 0);
+        copy16(dst + (16 + i * ROWS) * PITCH, vh + from, o >= 0);
+      }
+      return __ballot_sync(0xffffffffu, at >= 0) & 0xffffu;
+    };
 
     int kb = unit0 * kDecodeUnit + warp * 16;
-    int64_t at = place(kb);
+    int ahead = kb;                    // first entry of the next fetch
+    uint64_t exist = 0;                // 16 bits per stage in flight, the oldest lowest
+    int64_t at = place(ahead);
+#pragma unroll
+    for (int st = 0; st < S; ++st) {
+      const int64_t now = at;
+      const bool more = ahead < key1;
+      ahead += kDecodeUnit;
+      at = place(ahead);
+      if (more) exist |= static_cast<uint64_t>(fetch(st, now)) << (16 * st);
+      copy_commit();
+    }
+    int st = 0;
     for (; kb < key1; kb += kDecodeUnit) {
-      int64_t vo[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        vo[i] = __shfl_sync(0xffffffffu, at, 2 * t + (i & 1) + (i >> 1) * 8);
-      uint4 kf[2][NJ], vf[4][NH];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int64_t ko = __shfl_sync(0xffffffffu, at, r + 8 * i);
-#pragma unroll
-        for (int j = 0; j < NJ; ++j)
-          kf[i][j] = ko >= 0 ? ldg_stream(kh + ko + j * 64) : make_uint4(0, 0, 0, 0);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int h = 0; h < NH; ++h)
-          vf[i][h] = vo[i] >= 0 ? ldg_stream(vh + vo[i] + h * 128) : make_uint4(0, 0, 0, 0);
-      at = place(kb + kDecodeUnit);
-
-      // logits of entries 2t, 2t + 1 (first MMA tile) and 8 + 2t, 8 + 2t + 1 (second), head r
+      copy_wait<S - 1>();
+      __syncwarp();                    // the other lanes' copies of the stage have landed too
+      const uint32_t kst = ring + st * STAGE + t * 16;
+      const uint32_t vst = ring + st * STAGE + 16 * PITCH + r * 16;
+      // logits of head r for columns 2t, 2t + 1 of the first MMA tile and of the second
       float s[2][4];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
-          Elem<T>::mma(s[i], qf[j].x, 0u, qf[j].y, 0u, kf[i][j].x, kf[i][j].y);
-          Elem<T>::mma(s[i], qf[j].z, 0u, qf[j].w, 0u, kf[i][j].z, kf[i][j].w);
+          const uint4 kf = lds16(kst + (8 * i + entry_of(r >> 1, r & 1)) * PITCH + j * 64);
+          Elem<T>::mma(s[i], qf[j].x, 0u, qf[j].y, 0u, kf.x, kf.y);
+          Elem<T>::mma(s[i], qf[j].z, 0u, qf[j].w, 0u, kf.z, kf.w);
         }
       }
       float x[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        x[i] = vo[i] >= 0 ? s[i >> 1][i & 1] * p.scale_log2 : -INFINITY;
-      if (p.logits && r < rows) {
-        float *lg = p.logits + (static_cast<int64_t>(b) * c.hq + h0 + r) * p.cap64 + kb + 2 * t;
-        if (kb + 2 * t < key1) *reinterpret_cast<float2 *>(lg) = make_float2(x[0], x[1]);
-        if (kb + 8 + 2 * t < key1) *reinterpret_cast<float2 *>(lg + 8) = make_float2(x[2], x[3]);
+      for (int i = 0; i < 4; ++i) {
+        const int e = entry_of(t, i & 1) + (i >> 1) * 8;
+        x[i] = (exist >> e) & 1u ? s[i >> 1][i & 1] * p.scale_log2 : -INFINITY;
+        if (p.logits && r < rows && kb + e < key1)
+          p.logits[(static_cast<int64_t>(b) * c.hq + h0 + r) * p.cap64 + kb + e] = x[i];
       }
       float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
@@ -243,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 3)
           for (int q = 0; q < 4; ++q) acc[i][q] *= alpha;
       }
       const float base = m_run == -INFINITY ? 0.f : m_run;
-      float w[4], lo[4];
+      float w[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         w[i] = exp2f(x[i] - base);
@@ -251,17 +314,18 @@ __global__ void __launch_bounds__(kThreads, 3)
       }
       const uint32_t hi0 = Elem<T>::pack(w[0], w[1]), hi1 = Elem<T>::pack(w[2], w[3]);
       const float2 f0 = Elem<T>::unpack(hi0), f1 = Elem<T>::unpack(hi1);
-      lo[0] = w[0] - f0.x;
-      lo[1] = w[1] - f0.y;
-      lo[2] = w[2] - f1.x;
-      lo[3] = w[3] - f1.y;
-      const uint32_t lo0 = Elem<T>::pack(lo[0], lo[1]), lo1 = Elem<T>::pack(lo[2], lo[3]);
+      const uint32_t lo0 = Elem<T>::pack(w[0] - f0.x, w[1] - f0.y);
+      const uint32_t lo1 = Elem<T>::pack(w[2] - f1.x, w[3] - f1.y);
 #pragma unroll
       for (int h = 0; h < NH; ++h) {
-        const uint32_t *v0 = reinterpret_cast<const uint32_t *>(&vf[0][h]);
-        const uint32_t *v1 = reinterpret_cast<const uint32_t *>(&vf[1][h]);
-        const uint32_t *v2 = reinterpret_cast<const uint32_t *>(&vf[2][h]);
-        const uint32_t *v3 = reinterpret_cast<const uint32_t *>(&vf[3][h]);
+        uint4 vf[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          vf[i] = lds16(vst + (entry_of(t, i & 1) + (i >> 1) * 8) * PITCH + h * 128);
+        const uint32_t *v0 = reinterpret_cast<const uint32_t *>(&vf[0]);
+        const uint32_t *v1 = reinterpret_cast<const uint32_t *>(&vf[1]);
+        const uint32_t *v2 = reinterpret_cast<const uint32_t *>(&vf[2]);
+        const uint32_t *v3 = reinterpret_cast<const uint32_t *>(&vf[3]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const uint32_t pick = (e & 1) ? 0x7632u : 0x5410u;
@@ -270,7 +334,19 @@ __global__ void __launch_bounds__(kThreads, 3)
                        __byte_perm(v2[e >> 1], v3[e >> 1], pick));
         }
       }
+      // every lane's reads of the stage fed the MMAs above, so its rows can be filled again
+      __syncwarp();
+      exist >>= 16;
+      if (ahead < key1) {
+        exist |= static_cast<uint64_t>(fetch(st, at)) << (16 * (S - 1));
+        ahead += kDecodeUnit;
+        at = place(ahead);
+      }
+      copy_commit();
+      st = st + 1 == S ? 0 : st + 1;
     }
+    copy_wait<0>();
+    __syncwarp();
 
     // ---- the warps' results meet in shared memory
     l_run += __shfl_xor_sync(0xffffffffu, l_run, 1);
@@ -287,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 3)
       for (int q = 0; q < 2; ++q)
 #pragma unroll
         for (int e = 0; e < 8; e += 4)
-          *reinterpret_cast<float4 *>(&s_o[warp][r][h * 64 + t * 16 + q * 8 + e]) =
+          *reinterpret_cast<float4 *>(s_o(warp) + r * ROW + h * 64 + t * 16 + q * 8 + e) =
               make_float4(acc[h * 8 + e][q] + acc[h * 8 + e][q + 2],
                           acc[h * 8 + e + 1][q] + acc[h * 8 + e + 1][q + 2],
                           acc[h * 8 + e + 2][q] + acc[h * 8 + e + 2][q + 2],
@@ -310,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 3)
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float f = exp2f(s_m[w][row] - base);
-        const float4 x = *reinterpret_cast<const float4 *>(&s_o[w][row][col]);
+        const float4 x = *reinterpret_cast<const float4 *>(s_o(w) + row * ROW + col);
         l += f * s_l[w][row];
         o.x += f * x.x;
         o.y += f * x.y;
@@ -382,11 +458,16 @@ __global__ void __launch_bounds__(kThreads, 3)
   }
 }
 
-// weight[entry, KV head] += sum over the KV head's query heads of 2^(logit - lse2). One thread per
-// entry; the logits of the pass before are read once, most of them from L2.
-__global__ void __launch_bounds__(kThreads) add_weight_kernel(const __grid_constant__ DecodeParams p) {
+// weight[entry, KV head] += sum over the KV head's query heads of 2^(logit - lse2). A thread takes four
+// entries; the logits of the pass before are read once, most of them from L2.
+constexpr int kWeightThreads = 256;
+
+__global__ void __launch_bounds__(kWeightThreads)
+    add_weight_kernel(const __grid_constant__ DecodeParams p) {
   __shared__ int s_scan[20];
   const CacheView &c = p.c;
+  grid_dependency_wait();
+  grid_dependents_go();
   Cursor cur;
   int total;
   const int per = locate(c, c.hkv, gridDim.x, blockIdx.x, s_scan, &cur, &total);
@@ -399,42 +480,63 @@ __global__ void __launch_bounds__(kThreads) add_weight_kernel(const __grid_const
     const int n = min(cur.units - unit0, end - pos);
     const int key1 = min(cur.len, (unit0 + n) * kDecodeUnit);
     const int64_t row0 = static_cast<int64_t>(cur.b) * c.hq + head * c.g;
-    for (int e = unit0 * kDecodeUnit + threadIdx.x; e < key1; e += kThreads) {
-      int slot, off;
-      split_entry(c, e, slot, off);
-      const int pg = page_at(c, cur.b, slot);
-      if (pg < 0) continue;
-      float sum = 0.f;
+    for (int e = unit0 * kDecodeUnit + threadIdx.x * 4; e < key1; e += kWeightThreads * 4) {
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
       for (int h = 0; h < c.g; ++h) {
+        const float4 x = __ldcg(reinterpret_cast<const float4 *>(p.logits + (row0 + h) * p.cap64 + e));
         const float l2 = p.lse2[row0 + h];
-        const float x = p.logits[(row0 + h) * p.cap64 + e];
         // a row whose every logit is -inf has no weights
-        sum += l2 == -INFINITY ? 0.f : exp2f(x - l2);
+        const float base = l2 == -INFINITY ? INFINITY : l2;
+        sum[0] += exp2f(x.x - base);
+        sum[1] += exp2f(x.y - base);
+        sum[2] += exp2f(x.z - base);
+        sum[3] += exp2f(x.w - base);
       }
-      atomicAdd(c.weight + track_at(c, pg, head, off), sum);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (e + i >= key1) break;
+        int slot, off;
+        split_entry(c, e + i, slot, off);
+        const int pg = page_at(c, cur.b, slot);
+        if (pg >= 0) atomicAdd(c.weight + track_at(c, pg, head, off), sum[i]);
+      }
     }
     pos += n;
     if (pos < end && pos - cur.start == cur.units * c.hkv) next_sequence(c, c.hkv, &cur);
   }
 }
 
-template <class T>
+template <class T, int D>
 cudaError_t launch_decode_t(const DecodeParams &p, cudaStream_t stream) {
-  if (p.c.d == 128)
-    paged_decode_kernel<T, 128><<<p.grid, kThreads, 0, stream>>>(p);
-  else
-    paged_decode_kernel<T, 64><<<p.grid, kThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  // more than 48 KB of shared memory has to be allowed once per device
+  static std::atomic<uint64_t> allowed{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
+  if ((allowed.load(std::memory_order_relaxed) & bit) == 0) {
+    e = cudaFuncSetAttribute(paged_decode_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(kRingBytes<D>));
+    if (e != cudaSuccess) return e;
+    allowed.fetch_or(bit, std::memory_order_relaxed);
+  }
+  return launch_dependent(paged_decode_kernel<T, D>, dim3(p.grid), kThreads, kRingBytes<D>, 1, stream,
+                          p);
+}
+
+template <class T>
+cudaError_t launch_decode_d(const DecodeParams &p, cudaStream_t stream) {
+  return p.c.d == 128 ? launch_decode_t<T, 128>(p, stream) : launch_decode_t<T, 64>(p, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_decode(const DecodeParams &p, int dtype, int num_sms, cudaStream_t stream) {
-  cudaError_t e = dtype == RRA_BF16 ? launch_decode_t<__nv_bfloat16>(p, stream)
-                                    : launch_decode_t<__half>(p, stream);
+  const cudaError_t e = dtype == RRA_BF16 ? launch_decode_d<__nv_bfloat16>(p, stream)
+                                          : launch_decode_d<__half>(p, stream);
   if (e != cudaSuccess || !p.logits) return e;
-  add_weight_kernel<<<num_sms * 8, kThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_dependent(add_weight_kernel, dim3(num_sms * 6), kWeightThreads, 0, 1, stream, p);
 }
 
 }  // namespace rra

@@ -44,6 +44,8 @@ __device__ __forceinline__ void turn(const RopeUnit &r, uint4 &a, uint4 &b) {
 template <class T, bool ADJACENT, bool CACHED>
 __global__ void __launch_bounds__(256)
     rope_kernel(const __grid_constant__ RopeParams p, const __grid_constant__ CacheView c) {
+  grid_dependency_wait();
+  grid_dependents_go();
   const int units = p.d / 16;
   const int64_t idx = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   const int64_t row = idx / units;
@@ -143,19 +145,10 @@ __global__ void __launch_bounds__(256)
 template <class T>
 static cudaError_t launch_rope_t(const RopeParams &p, const CacheView *cache, int pairing,
                                  dim3 grid, cudaStream_t stream) {
-  const CacheView none{};
-  if (pairing == RRA_PAIRS_ADJACENT) {
-    if (cache)
-      rope_kernel<T, true, true><<<grid, 256, 0, stream>>>(p, *cache);
-    else
-      rope_kernel<T, true, false><<<grid, 256, 0, stream>>>(p, none);
-  } else {
-    if (cache)
-      rope_kernel<T, false, true><<<grid, 256, 0, stream>>>(p, *cache);
-    else
-      rope_kernel<T, false, false><<<grid, 256, 0, stream>>>(p, none);
-  }
-  return cudaGetLastError();
+  const bool adjacent = pairing == RRA_PAIRS_ADJACENT;
+  const auto kern = cache ? (adjacent ? rope_kernel<T, true, true> : rope_kernel<T, false, true>)
+                          : (adjacent ? rope_kernel<T, true, false> : rope_kernel<T, false, false>);
+  return launch_dependent(kern, grid, 256, 0, 1, stream, p, cache ? *cache : CacheView{});
 }
 
 cudaError_t launch_rope(const RopeParams &in, const CacheView *cache, int dtype, int pairing,

@@ -4,6 +4,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "cache_internal.h"
 
@@ -16,12 +17,13 @@ CacheLayout cache_layout(const CacheView &c, bool tracked, int num_sms) {
   w.head_tiles = (c.g + kDecodeHeads - 1) / kDecodeHeads;
   const int64_t items = static_cast<int64_t>(c.batch) * c.hkv * w.head_tiles;
   w.cap64 = (static_cast<int64_t>(c.cap) + kDecodeUnit - 1) / kDecodeUnit * kDecodeUnit;
-  // three CTAs fit an SM; no more than there can be units of work
+  // one CTA for every place on the SMs, but no more than there can be units of work
   const int64_t most = items * (w.cap64 / kDecodeUnit);
-  w.grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(num_sms * 3, most)));
+  w.grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(num_sms * decode_ctas(c.d), most)));
   size_t off = 256;
   w.status = 0;
   w.done = 4;
+  w.epoch = 8;
   w.counters = off;
   off = align_up(off + items * 4, 256);
   w.part_ml = off;
@@ -33,10 +35,14 @@ CacheLayout cache_layout(const CacheView &c, bool tracked, int num_sms) {
   if (tracked) {
     w.skip = off;
     off = align_up(off + static_cast<size_t>(c.batch) * 4, 256);
+    w.tags = off;
+    off = align_up(off + static_cast<size_t>(c.batch) * 4, 256);
+    w.lens = off;
+    off = align_up(off + static_cast<size_t>(c.batch) * 4, 256);
     w.plan = off;
-    off = align_up(off + static_cast<size_t>(c.batch) * (c.hkv + 1) * 4, 256);
+    off = align_up(off + static_cast<size_t>(c.batch) * c.hkv * 4, 256);
     w.owner = off;
-    off = align_up(off + static_cast<size_t>(c.num_pages) * 4, 256);
+    off = align_up(off + static_cast<size_t>(c.num_pages) * 8, 256);
     w.big = off;
     w.moves = c.cap / 2 + 1;   // a list holds at most min(budget, len - budget) entries
     const size_t logits = static_cast<size_t>(c.batch) * c.hq * w.cap64 * 4;
@@ -58,10 +64,14 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 bool row_stride(int64_t s) { return s >= 0 && s % 8 == 0; }
 
+// SMs of the current device (asked once per device).
 int current_sms() {
+  static std::atomic<int> cache[64];
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return -1;
+  if (dev >= 0 && dev < 64 && (n = cache[dev].load(std::memory_order_relaxed)) > 0) return n;
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return -1;
+  if (dev >= 0 && dev < 64) cache[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 
@@ -377,9 +387,12 @@ rra_status rra_cache_evict(const rra_cache *cache, int budget, int sinks, int re
   p.sinks = sinks;
   p.recent = recent;
   p.advance = advance != 0;
-  p.skip = at<int32_t>(cache->workspace, w.skip);
+  p.epoch = at<uint32_t>(cache->workspace, w.epoch);
+  p.skip = at<uint32_t>(cache->workspace, w.skip);
+  p.tags = at<uint32_t>(cache->workspace, w.tags);
+  p.lens = at<int32_t>(cache->workspace, w.lens);
   p.plan = at<int32_t>(cache->workspace, w.plan);
-  p.owner = at<int32_t>(cache->workspace, w.owner);
+  p.owner = at<unsigned long long>(cache->workspace, w.owner);
   p.moves = at<int32_t>(cache->workspace, w.big);
   p.moves_cap = w.moves;
   return cuda_status(rra::launch_evict(p, sms, reinterpret_cast<cudaStream_t>(stream)));

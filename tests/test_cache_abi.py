@@ -42,6 +42,14 @@ def test_struct_layouts():
     assert ctypes.sizeof(cache._Tokens) == 24 + 32 + 6 * 32
     assert cache._Cache.page_stride.offset == 40 and cache._Cache.k.offset == 72
     assert ctypes.sizeof(cache._Cache) == 144
+    # the packed forms that the binding passes are these structs
+    t = cache._Tokens.from_buffer_copy(cache._pack_tokens(1, 2, 3, 4, 1, *range(10, 38)))
+    assert (t.batch, t.heads_q, t.heads_kv, t.tokens, t.dtype) == (1, 2, 3, 4, 1)
+    assert (t.positions.data, t.positions.token) == (10, 13)
+    assert (t.q.data, t.k.batch, t.v.head, t.q_out.token) == (14, 19, 24, 29)
+    assert (t.k_out.data, t.v_out.token) == (30, 37)
+    v = cache._View.from_buffer_copy(cache._pack_view(5, 6, 7, 8))
+    assert (v.data, v.batch, v.head, v.token) == (5, 6, 7, 8)
 
 
 # ------------------------------------------------------------------------------------ rope tables
