@@ -28,13 +28,8 @@ __device__ __forceinline__ int cache_len(const CacheView &c, int b) {
 }
 
 __device__ __forceinline__ void split_entry(const CacheView &c, int e, int &slot, int &off) {
-  if (c.ps_shift >= 0) {
-    slot = e >> c.ps_shift;
-    off = e & (c.ps - 1);
-  } else {
-    slot = static_cast<int>(static_cast<unsigned>(e) / static_cast<unsigned>(c.ps));
-    off = e - slot * c.ps;
-  }
+  slot = static_cast<int>(__umulhi(static_cast<uint32_t>(e) * 2u, c.ps_magic) >> c.ps_shift);
+  off = e - slot * c.ps;
 }
 
 // Page of table place `slot` of sequence b, or -1 (flagged) if it is not a page of the cache.

@@ -2,8 +2,8 @@
 // entries (the first tokens and the last ones, by their ordinals) and then those of the largest
 // weight, `budget` in all. Two launches:
 //
-//   select  a cluster of CTAs per (sequence, KV head) finds the budget-th largest key by a radix
-//           descent (11, 11 and 10 bits; the histograms are summed over the cluster through
+//   select  a block or a cluster per (sequence, KV head) finds the budget-th largest key by a radix
+//           descent (digits of 8 bits; the histograms are summed over the cluster through
 //           distributed shared memory) and lists the evicted places e < budget and the kept
 //           entries e >= budget, both in ascending order: there are as many of one as of the other.
 //           Along the way it claims the sequences' pages: a page claimed twice in a call is named twice by
@@ -17,6 +17,7 @@
 #include <cooperative_groups.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "cache_device.cuh"
 
@@ -26,276 +27,364 @@ namespace cg = cooperative_groups;
 
 namespace {
 
+constexpr int kBins = 256;
+constexpr int kPasses = 4;         // digits of 8, 8, 8 and 7 bits from bit 30 down
+constexpr uint32_t kProtected = 0x7fffffffu;
 constexpr int kSelThreads = 512;
-constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kBins = 2048;
+constexpr int kKeyRoom = 16384;    // keys that a CTA of a cluster holds in shared memory, 64 KB
 constexpr int kMoveWarps = 8;
 
 // Orders entries by what is kept first: protected entries, then the weight. Weights that are not
-// above zero are 0; positive floats order like their bits.
+// above zero are 0; positive floats order like their bits, infinity is 0x7f800000. 31 bits.
 __device__ __forceinline__ uint32_t entry_key(const EvictParams &p, int32_t order, float w,
                                               int64_t recent_from) {
-  if (order < p.sinks || order >= recent_from) return 0xffffffffu;
+  if (order < p.sinks || order >= recent_from) return kProtected;
   return w > 0.f ? __float_as_uint(w) : 0u;
 }
 
-// All threads of the cluster; of the block where it is alone.
-__device__ __forceinline__ void sync_all(cg::cluster_group &cl, int ranks) {
-  if (ranks > 1)
-    cl.sync();
-  else
-    __syncthreads();
+// What a sequence is cut by.
+struct Cut {
+  int n;               // entries
+  uint32_t tag;        // the call's mark, one above the count of calls (the move kernel moves that on)
+  int64_t recent_from; // ordinals from here on are protected
+};
+
+__device__ __forceinline__ Cut read_cut(const EvictParams &p, int b, bool first) {
+  const CacheView &c = p.c;
+  const int raw = c.len[b];
+  Cut cut;
+  cut.tag = *p.epoch + 1u;
+  cut.recent_from = static_cast<int64_t>(c.seen[b]) - p.recent;
+  cut.n = raw < 0 ? 0 : min(raw, c.cap);
+  if (first) {
+    if (raw != cut.n) raise(c.status, kErrBadLength);
+    p.lens[b] = cut.n;
+    p.tags[b] = cut.tag;
+  }
+  return cut;
 }
 
-// Exclusive prefix of `mine` over the warps of the block, then over the CTAs of the cluster before
-// this one. s_warp: [kSelWarps], s_cta: one word that the other CTAs read.
-__device__ int2 exclusive(cg::cluster_group &cl, int2 mine, int2 *s_warp, int2 *s_cta) {
+// Claims the pages `part`, `part` + `parts`, ... of the sequence. A page that comes back with this
+// call's tag was claimed before: both of its sequences stay as they are.
+__device__ __forceinline__ void claim_pages(const EvictParams &p, int b, const Cut &cut, int part,
+                                            int parts) {
+  const CacheView &c = p.c;
+  const int pages = (cut.n + c.ps - 1) / c.ps;
+  for (int i = part; i < pages; i += parts) {
+    const int pg = page_at(c, b, i);
+    if (pg < 0) {
+      p.skip[b] = cut.tag;
+      continue;
+    }
+    const unsigned long long me =
+        (static_cast<unsigned long long>(cut.tag) << 32) | static_cast<unsigned>(b);
+    const unsigned long long was = atomicExch(p.owner + pg, me);
+    if (static_cast<uint32_t>(was >> 32) == cut.tag) {
+      p.skip[b] = cut.tag;
+      p.skip[static_cast<uint32_t>(was)] = cut.tag;
+      raise(c.status, kErrSharedPage);
+    }
+  }
+}
+
+// Sum over the lanes below, of x.
+__device__ __forceinline__ uint32_t lane_prefix(uint32_t x, int lane) {
+  uint32_t incl = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  return incl - x;
+}
+
+__device__ __forceinline__ int digit_shift(int pass) { return pass == 3 ? 0 : 23 - 8 * pass; }
+
+// What the descent has found: `prefix` holds the digits of the want-th largest key so far, `ties` the
+// keys that share them.
+struct Found {
+  uint32_t prefix, want, ties;
+};
+
+// One digit. Every warp searches the bins for itself (lane i holds eight of them, from the top).
+// Returns false if the bins hold fewer than f->want keys, which are taken off f->want.
+__device__ __forceinline__ bool descend(const uint32_t *bins, int pass, Found *f) {
+  const int lane = threadIdx.x & 31;
+  const int top = kBins - 8 - 8 * lane;
+  const uint4 hi = *reinterpret_cast<const uint4 *>(bins + top + 4);
+  const uint4 lo = *reinterpret_cast<const uint4 *>(bins + top);
+  const uint32_t cnt[8] = {hi.w, hi.z, hi.y, hi.x, lo.w, lo.z, lo.y, lo.x};
+  uint32_t sum = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sum += cnt[i];
+  const uint32_t before = lane_prefix(sum, lane);
+  const uint32_t here = __ballot_sync(0xffffffffu, before < f->want && f->want <= before + sum);
+  if (here == 0) {
+    f->want -= __shfl_sync(0xffffffffu, before + sum, 31);
+    return false;
+  }
+  uint32_t passed = before, above = before, mine = 0, ties = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (passed < f->want) {      // the last bin that satisfies this is the one
+      mine = i;
+      above = passed;
+      ties = cnt[i];
+    }
+    passed += cnt[i];
+  }
+  const int from = __ffs(here) - 1;
+  f->want -= __shfl_sync(0xffffffffu, above, from);
+  f->ties = __shfl_sync(0xffffffffu, ties, from);
+  f->prefix |= __shfl_sync(0xffffffffu, static_cast<uint32_t>(top) + 7u - mine, from)
+               << digit_shift(pass);
+  return true;
+}
+
+// Prefix of the warps' values `mine` over the block, and with CLUSTER over the CTAs before this one too.
+// s_warp: [WARPS]; s_cta: a pair that the other CTAs read.
+template <int WARPS, bool CLUSTER>
+__device__ __forceinline__ int2 prefix_of_warps(int2 mine, int2 *s_warp, int2 *s_cta, int2 *all) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (lane == 0) s_warp[warp] = mine;
   __syncthreads();
-  int2 before = make_int2(0, 0), all = make_int2(0, 0);
-  for (int w = 0; w < kSelWarps; ++w) {
-    const int2 x = s_warp[w];
-    if (w < warp) {
-      before.x += x.x;
-      before.y += x.y;
-    }
-    all.x += x.x;
-    all.y += x.y;
-  }
-  if (cl.num_blocks() == 1) return before;
-  if (threadIdx.x == 0) *s_cta = all;
-  cl.sync();
-  for (unsigned k = 0; k < cl.block_rank(); ++k) {
-    const int2 x = *cl.map_shared_rank(s_cta, k);
-    before.x += x.x;
-    before.y += x.y;
+  const int2 v = lane < WARPS ? s_warp[lane] : make_int2(0, 0);
+  const int x = static_cast<int>(lane_prefix(v.x, lane)), y = static_cast<int>(lane_prefix(v.y, lane));
+  *all = make_int2(__shfl_sync(0xffffffffu, x + v.x, 31), __shfl_sync(0xffffffffu, y + v.y, 31));
+  int2 before = make_int2(__shfl_sync(0xffffffffu, x, warp), __shfl_sync(0xffffffffu, y, warp));
+  if (CLUSTER) {
+    cg::cluster_group cl = cg::this_cluster();
+    if (threadIdx.x == 0) *s_cta = *all;
+    cl.sync();
+    const int ranks = cl.num_blocks(), rank = cl.block_rank();
+    const int2 z = lane < ranks ? *cl.map_shared_rank(s_cta, lane) : make_int2(0, 0);
+    const int zx = static_cast<int>(lane_prefix(z.x, lane)), zy = static_cast<int>(lane_prefix(z.y, lane));
+    before.x += __shfl_sync(0xffffffffu, zx, rank);
+    before.y += __shfl_sync(0xffffffffu, zy, rank);
+    *all = make_int2(__shfl_sync(0xffffffffu, zx, 31), __shfl_sync(0xffffffffu, zy, 31));
   }
   return before;
 }
 
-// KPT: keys that a thread holds in registers; a CTA's share of more than KPT * kSelThreads entries is
-// taken in rounds and read again for every digit.
-template <int KPT>
-__global__ void __launch_bounds__(kSelThreads)
-    evict_select_kernel(const __grid_constant__ EvictParams p) {
-  __shared__ __align__(16) uint32_t s_hist[3][kBins];
-  __shared__ uint32_t s_scan[kSelWarps];
-  __shared__ int2 s_warp[2][kSelWarps];
-  __shared__ int2 s_cta[2];
-  __shared__ uint32_t s_found[3];
+// Keys of the entries e0 + 32 i + lane, i < count, to keys[32 i + lane]; entries at or past `end` get
+// key 0. The pages of a batch are looked up together, then its weights and ordinals; a page that is
+// none (the sequence is left alone) reads as page 0. Returns the protected entries of the warp.
+__device__ __noinline__ int load_keys(const EvictParams &p, int b, int head, int64_t recent_from,
+                                      int e0, int end, int count, uint32_t *keys) {
+  constexpr int BATCH = 4;
+  const CacheView &c = p.c;
+  int safe = 0;
+  const int lane = threadIdx.x & 31;
+  const int32_t *table = c.table + b * c.table_stride;
+#pragma unroll 1
+  for (int i = 0; i < count; i += BATCH) {
+    int page[BATCH];
+    int32_t order[BATCH];
+    float w[BATCH];
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      if (i + k >= count) break;
+      int slot, off;
+      split_entry(c, min(e0 + (i + k) * 32 + lane, end - 1), slot, off);
+      page[k] = table[slot];
+    }
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      if (i + k >= count) break;
+      int slot, off;
+      split_entry(c, min(e0 + (i + k) * 32 + lane, end - 1), slot, off);
+      const int pg = static_cast<unsigned>(page[k]) < static_cast<unsigned>(c.num_pages) ? page[k] : 0;
+      const int64_t at = track_at(c, pg, head, off);
+      order[k] = __ldcg(c.order + at);
+      w[k] = __ldcg(c.weight + at);
+    }
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      if (i + k >= count) break;
+      const uint32_t key =
+          e0 + (i + k) * 32 + lane < end ? entry_key(p, order[k], w[k], recent_from) : 0u;
+      keys[(i + k) * 32 + lane] = key;
+      safe += __popc(__ballot_sync(0xffffffffu, key == kProtected));
+    }
+  }
+  return safe;
+}
+
+// One block, or one cluster of blocks, per (sequence, KV head). room: keys that the dynamic shared
+// memory holds; a CTA's share of more entries is taken in rounds and read again for every digit. Loops are
+// kept rolled: a short call is bound by latencies, instruction fetches among them.
+template <int THREADS, bool CLUSTER>
+__global__ void __launch_bounds__(THREADS, 2)
+    evict_select_kernel(const __grid_constant__ EvictParams p, int room) {
+  constexpr int WARPS = THREADS / 32;
+  extern __shared__ uint32_t s_keys[];
+  __shared__ __align__(16) uint32_t s_hist[kPasses][kBins], s_sum[2][kBins];
+  __shared__ uint32_t s_safe;
+  __shared__ int2 s_warp[2][WARPS];
+  __shared__ int2 s_cta[3];
 
   const CacheView &c = p.c;
   cg::cluster_group cl = cg::this_cluster();
-  const int ranks = cl.num_blocks(), rank = cl.block_rank();
+  const int ranks = CLUSTER ? cl.num_blocks() : 1, rank = CLUSTER ? cl.block_rank() : 0;
   const int item = blockIdx.x / ranks;
   const int b = item / c.hkv, head = item - b * c.hkv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  for (int i = tid; i < 3 * kBins / 4; i += kSelThreads)
-    reinterpret_cast<uint4 *>(&s_hist[0][0])[i] = make_uint4(0, 0, 0, 0);
+  for (int i = tid; i < kPasses * kBins; i += THREADS) (&s_hist[0][0])[i] = 0;
+  if (tid == 0) s_safe = 0;
   grid_dependency_wait();
   grid_dependents_go();
-  const int raw = c.len[b];
-  const uint32_t tag = *p.epoch + 1u;   // the same for the whole call; the move kernel moves it on
-  const int64_t recent_from = static_cast<int64_t>(c.seen[b]) - p.recent;
-  const int n = raw < 0 ? 0 : min(raw, c.cap);
-  if (rank == 0 && head == 0 && tid == 0) {
-    if (raw != n) raise(c.status, kErrBadLength);
-    p.lens[b] = n;
-    p.tags[b] = tag;
-  }
-  // The pages of the sequence, shared out over its heads. A page that comes back with this call's tag was
-  // claimed before: both of its sequences stay as they are.
-  const int pages = (n + c.ps - 1) / c.ps;
-  for (int i = (head * ranks + rank) * kSelThreads + tid; i < pages;
-       i += c.hkv * ranks * kSelThreads) {
-    const int pg = page_at(c, b, i);
-    if (pg < 0) {
-      p.skip[b] = tag;
-      continue;
-    }
-    const unsigned long long me =
-        (static_cast<unsigned long long>(tag) << 32) | static_cast<unsigned>(b);
-    const unsigned long long was = atomicExch(p.owner + pg, me);
-    if (static_cast<uint32_t>(was >> 32) == tag) {
-      p.skip[b] = tag;
-      p.skip[static_cast<uint32_t>(was)] = tag;
-      raise(c.status, kErrSharedPage);
-    }
-  }
-  if (n <= p.budget) {   // the same for the whole cluster
-    if (rank == 0 && tid == 0) p.plan[item] = 0;
-    return;
-  }
-
-  // each CTA takes a run of entries, each of its warps a run of those
-  const int per_warp = ((n + ranks * kSelWarps - 1) / (ranks * kSelWarps) + 31) / 32 * 32;
-  const int wlo = min((rank * kSelWarps + warp) * per_warp, n), whi = min(wlo + per_warp, n);
-  const int rounds = (per_warp + KPT * 32 - 1) / (KPT * 32);
-  uint32_t key[KPT];
-  // key[k] of entry wlo + (round * KPT + k) * 32 + lane. The pages of a batch are looked up together, then
-  // its weights and ordinals; a page that is none (the sequence is left alone) reads as page 0.
-  auto load = [&](int round) {
-    constexpr int BATCH = KPT < 8 ? KPT : 8;
-    const int e0 = wlo + round * KPT * 32 + lane;
-#pragma unroll
-    for (int k0 = 0; k0 < KPT; k0 += BATCH) {
-      int64_t at[BATCH];
-      int32_t order[BATCH];
-      float w[BATCH];
-#pragma unroll
-      for (int k = 0; k < BATCH; ++k) {
-        const int e = min(e0 + (k0 + k) * 32, n - 1);
-        int slot, off;
-        split_entry(c, e, slot, off);
-        const int pg = c.table[b * c.table_stride + slot];
-        at[k] = track_at(c, static_cast<unsigned>(pg) < static_cast<unsigned>(c.num_pages) ? pg : 0,
-                         head, off);
+  const Cut cut = read_cut(p, b, rank == 0 && head == 0 && tid == 0);
+  const int n = cut.n;
+  int moves = 0;
+  if (n > p.budget) {   // the same for the whole cluster
+    // each CTA takes a run of entries, each of its warps a run of those, in rounds of `take` rows of 32
+    const int per_warp = (n + ranks * THREADS - 1) / (ranks * THREADS) * 32;
+    const int wlo = min((rank * WARPS + warp) * per_warp, n), whi = min(wlo + per_warp, n);
+    const int take = room / THREADS;
+    const int rounds = (per_warp / 32 + take - 1) / take;
+    uint32_t *keys = s_keys + warp * take * 32;
+    int safe = 0;
+    // rows of a round, after reading its keys unless they are there
+    auto rows_of = [&](int round, bool first) {
+      const int e0 = wlo + round * take * 32;
+      const int rows = (max(0, min(whi - e0, take * 32)) + 31) / 32;
+      if (first || rounds > 1) {
+        __syncwarp();
+        const int found = load_keys(p, b, head, cut.recent_from, e0, whi, rows, keys);
+        if (first) safe += found;
       }
-#pragma unroll
-      for (int k = 0; k < BATCH; ++k) {
-        order[k] = __ldcg(c.order + at[k]);
-        w[k] = __ldcg(c.weight + at[k]);
-      }
-#pragma unroll
-      for (int k = 0; k < BATCH; ++k) key[k0 + k] = entry_key(p, order[k], w[k], recent_from);
-    }
-  };
-  load(0);
-  __syncthreads();
+      return rows;
+    };
 
-  uint32_t want = p.budget;    // the want-th largest key among those that match the digits so far
-  uint32_t prefix = 0;
-  uint32_t ties = 0;           // keys equal to the found one
+    // protected entries are counted apart, and entries of weight 0 not at all: both come in numbers
+    for (int round = 0; round < rounds; ++round) rows_of(round, true);
+    __syncthreads();
+    if (lane == 0) atomicAdd(&s_safe, static_cast<uint32_t>(safe));
+
+    Found f{0u, static_cast<uint32_t>(p.budget), 0u};
+    bool exact = false;        // the keys at or above the prefix are as many as wanted
 #pragma unroll 1
-  for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
-    const uint32_t digit = pass == 2 ? 0x3ffu : 0x7ffu;
-    const uint32_t mask = pass == 0 ? 0u : (pass == 1 ? 0xffe00000u : 0xfffffc00u);
-    uint32_t *hist = s_hist[pass];
-    for (int round = 0; round < rounds; ++round) {
-      if (rounds > 1) load(round);
-      const int e0 = wlo + round * KPT * 32 + lane;
-#pragma unroll
-      for (int k = 0; k < KPT; ++k) {
-        const bool in = e0 + k * 32 < whi && (key[k] & mask) == prefix;
-        const uint32_t votes = __ballot_sync(0xffffffffu, in);
-        if (votes == 0) continue;
-        // one add where all the lanes agree (equal weights, protected runs), else one per lane
-        const uint32_t bin = (key[k] >> shift) & digit;
-        const int first = __ffs(votes) - 1;
-        const uint32_t lead = __shfl_sync(0xffffffffu, bin, first);
-        if (__all_sync(0xffffffffu, !in || bin == lead)) {
-          if (lane == first) atomicAdd(&hist[bin], static_cast<uint32_t>(__popc(votes)));
-        } else if (in) {
-          atomicAdd(&hist[bin], 1u);
+    for (int pass = 0; pass < kPasses && !exact; ++pass) {
+      const int shift = digit_shift(pass), bits = pass == kPasses - 1 ? 7 : 8;
+      for (int round = 0; round < rounds; ++round) {
+        const int rows = rows_of(round, false);
+#pragma unroll 4
+        for (int i = 0; i < rows; ++i) {
+          const uint32_t key = keys[i * 32 + lane];
+          if (key != 0 && key != kProtected && ((key ^ f.prefix) >> (shift + bits)) == 0)
+            atomicAdd(&s_hist[pass][(key >> shift) & ((1u << bits) - 1u)], 1u);
         }
       }
-    }
-    sync_all(cl, ranks);
-    // thread i holds the bins from the top: kBins - 1 - 4 i and the three below it
-    uint32_t cnt[4] = {0, 0, 0, 0};
-    const int top = kBins - 1 - 4 * tid;
-    for (int k = 0; k < ranks; ++k) {
-      const uint32_t *h = cl.map_shared_rank(hist, k);
-      const uint4 x = *reinterpret_cast<const uint4 *>(h + top - 3);
-      cnt[0] += x.w;
-      cnt[1] += x.z;
-      cnt[2] += x.y;
-      cnt[3] += x.x;
-    }
-    const uint32_t sum = cnt[0] + cnt[1] + cnt[2] + cnt[3];
-    uint32_t incl = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t x = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += x;
-    }
-    if (lane == 31) s_scan[warp] = incl;
-    __syncthreads();
-    uint32_t above = incl - sum;
-#pragma unroll
-    for (int w = 0; w < kSelWarps; ++w) above += w < warp ? s_scan[w] : 0u;
-    if (above < want && want <= above + sum) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (above < want && want <= above + cnt[k]) {
-          s_found[0] = static_cast<uint32_t>(top - k) << shift;
-          s_found[1] = want - above;
-          s_found[2] = cnt[k];
+      const uint32_t *bins = s_hist[pass];
+      if (CLUSTER) {
+        cl.sync();
+        if (tid < kBins) {
+          uint32_t sum = 0;
+          for (int k = 0; k < ranks; ++k) sum += *cl.map_shared_rank(&s_hist[pass][tid], k);
+          s_sum[pass & 1][tid] = sum;
         }
-        above += cnt[k];
+        bins = s_sum[pass & 1];
       }
+      uint32_t kept_safe = 0;
+      if (CLUSTER && pass == 0)
+        for (int k = 0; k < ranks; ++k) kept_safe += *cl.map_shared_rank(&s_safe, k);
+      __syncthreads();
+      if (pass == 0) {
+        if (!CLUSTER) kept_safe = s_safe;
+        if (kept_safe >= f.want) {         // more protected entries than places: the first of them
+          f.prefix = kProtected;
+          f.ties = kept_safe;
+          exact = kept_safe == f.want;
+          break;
+        }
+        f.want -= kept_safe;
+      }
+      if (!descend(bins, pass, &f)) break;   // every weight above 0 stays, and the first of the zeros
+      exact = f.want == f.ties;
     }
-    __syncthreads();
-    prefix |= s_found[0];
-    want = s_found[1];
-    ties = s_found[2];
-  }
-
-  // keys above `prefix` are kept, and the first `want` of the `ties` equal ones
-  int tie_rank = 0;
-  const bool some = want < ties;
-  if (some) {
-    int mine = 0;
-    for (int round = 0; round < rounds; ++round) {
-      if (rounds > 1) load(round);
-      const int e0 = wlo + round * KPT * 32 + lane;
-#pragma unroll
-      for (int k = 0; k < KPT; ++k)
-        mine += __popc(__ballot_sync(0xffffffffu, e0 + k * 32 < whi && key[k] == prefix));
+    if (exact && f.prefix == 0) f.prefix = 1;   // the zeros were not counted
+    // kept: the keys at or above the prefix if exact, else those above it and the first f.want of those
+    // equal to it
+    int tie_rank = 0;
+    int2 all;
+    if (!exact) {
+      int ties = 0;
+      for (int round = 0; round < rounds; ++round) {
+        const int rows = rows_of(round, false), e0 = wlo + round * take * 32 + lane;
+        for (int i = 0; i < rows; ++i)
+          ties += __popc(__ballot_sync(0xffffffffu, e0 + i * 32 < whi && keys[i * 32 + lane] == f.prefix));
+      }
+      tie_rank = prefix_of_warps<WARPS, CLUSTER>(make_int2(ties, 0), s_warp[0], &s_cta[0], &all).x;
     }
-    tie_rank = exclusive(cl, make_int2(mine, 0), s_warp[0], &s_cta[0]).x;
-  }
-  const uint32_t below = (1u << lane) - 1u;
-  int32_t *holes = p.moves + static_cast<int64_t>(item) * 2 * p.moves_cap;
-  int32_t *movers = holes + p.moves_cap;
-  int2 at = make_int2(0, 0);
-#pragma unroll 1
-  for (int write = 0; write < 2; ++write) {
+    // Rows of 32: `kept` as a mask, which against the budget gives the places to fill and the entries to
+    // move. The masks are kept in the place of the row's first keys for the second pass, when the ranks of
+    // the first are known.
+    const uint32_t below = (1u << lane) - 1u;
+    int32_t *holes = p.moves + static_cast<int64_t>(item) * 2 * p.moves_cap;
+    int32_t *movers = holes + p.moves_cap;
     int rank_now = tie_rank;
+    auto masks = [&](int e0, int i) {
+      const int first = e0 + i * 32;
+      const uint32_t key = keys[i * 32 + lane];
+      const uint32_t in = whi - first >= 32 ? 0xffffffffu : (1u << (whi - first)) - 1u;
+      const uint32_t front =
+          p.budget >= first + 32 ? 0xffffffffu : (p.budget > first ? (1u << (p.budget - first)) - 1u : 0u);
+      uint32_t kept = __ballot_sync(0xffffffffu, exact ? key >= f.prefix : key > f.prefix) & in;
+      if (!exact) {
+        const uint32_t tied = __ballot_sync(0xffffffffu, key == f.prefix) & in;
+        kept |= __ballot_sync(0xffffffffu, ((tied >> lane) & 1u) != 0 &&
+                                               rank_now + __popc(tied & below) <
+                                                   static_cast<int>(f.want));
+        rank_now += __popc(tied);
+      }
+      return make_uint2(in & front & ~kept, kept & ~front);
+    };
     int2 seen = make_int2(0, 0);
     for (int round = 0; round < rounds; ++round) {
-      if (rounds > 1) load(round);
-      const int e0 = wlo + round * KPT * 32 + lane;
-#pragma unroll
-      for (int k = 0; k < KPT; ++k) {
-        const int e = e0 + k * 32;
-        const bool in = e < whi;
-        const bool tie = in && key[k] == prefix;
-        const uint32_t tied = __ballot_sync(0xffffffffu, tie);
-        const bool kept =
-            in && (key[k] > prefix ||
-                   (tie && (!some || rank_now + __popc(tied & below) < static_cast<int>(want))));
-        rank_now += __popc(tied);
-        const bool hole = in && !kept && e < p.budget, mover = kept && e >= p.budget;
-        const uint32_t hs = __ballot_sync(0xffffffffu, hole);
-        const uint32_t ms = __ballot_sync(0xffffffffu, mover);
-        if (write) {
-          if (hole) holes[at.x + seen.x + __popc(hs & below)] = e;
-          if (mover) movers[at.y + seen.y + __popc(ms & below)] = e;
-        }
-        seen.x += __popc(hs);
-        seen.y += __popc(ms);
+      const int rows = rows_of(round, false), e0 = wlo + round * take * 32;
+      for (int i = 0; i < rows; ++i) {
+        const uint2 m = masks(e0, i);
+        seen.x += __popc(m.x);
+        seen.y += __popc(m.y);
+        if (rounds == 1 && lane < 2) keys[i * 32 + lane] = lane == 0 ? m.x : m.y;
       }
     }
-    if (!write) {
-      at = exclusive(cl, seen, s_warp[1], &s_cta[1]);
-    } else if (rank == ranks - 1 && tid == kSelThreads - 1) {
-      p.plan[item] = at.x + seen.x;
+    int2 to = prefix_of_warps<WARPS, CLUSTER>(seen, s_warp[1], &s_cta[1], &all);
+    moves = all.x;
+    rank_now = tie_rank;
+    for (int round = 0; round < rounds; ++round) {
+      const int rows = rows_of(round, false), e0 = wlo + round * take * 32;
+      for (int i = 0; i < rows; ++i) {
+        const uint2 m = rounds == 1 ? make_uint2(keys[i * 32], keys[i * 32 + 1]) : masks(e0, i);
+        if ((m.x | m.y) == 0) continue;
+        if (((m.x | m.y) >> lane) & 1u) {
+          int slot, off;
+          split_entry(c, e0 + i * 32 + lane, slot, off);
+          // (page, place) as one number; a sequence with a bad page is left alone
+          const int row = c.table[b * c.table_stride + slot] * c.ps + off;
+          if ((m.x >> lane) & 1u)
+            holes[to.x + __popc(m.x & below)] = row;
+          else
+            movers[to.y + __popc(m.y & below)] = row;
+        }
+        to.x += __popc(m.x);
+        to.y += __popc(m.y);
+      }
     }
   }
-  if (ranks > 1) cl.sync();   // no CTA leaves while another reads its shared memory
+  if (rank == 0 && tid == 0) p.plan[item] = moves;
+  claim_pages(p, b, cut, (head * ranks + rank) * THREADS + tid, c.hkv * ranks * THREADS);
+  if (CLUSTER) cl.sync();   // no CTA leaves while another reads its shared memory
 }
 
 // A warp takes kFlight moves (twice as many for head_dim 64, whose two rows fill half a warp) of a
-// (sequence, KV head) at a time: as many lanes find the places of one each and move its weight and
-// ordinal, then the warp copies the rows, all loads before the first store.
+// (sequence, KV head) at a time: as many lanes move a weight and an ordinal each, then the warp copies the
+// rows, all loads before the first store; the next places are read while the rows are on their way.
 constexpr int kFlight = 8;
 
 template <int D>
-__global__ void __launch_bounds__(kMoveWarps * 32)
+__global__ void __launch_bounds__(kMoveWarps * 32, 4)
     evict_move_kernel(const __grid_constant__ EvictParams p, int parts) {
   constexpr int VECS = D / 8;                  // 16-byte vectors of a row
   constexpr int PER = 32 / (2 * VECS);         // moves whose key and value rows fill a warp: 1 or 2
@@ -320,32 +409,48 @@ __global__ void __launch_bounds__(kMoveWarps * 32)
     const int32_t *holes = p.moves + static_cast<int64_t>(item) * 2 * p.moves_cap;
     const int32_t *movers = holes + p.moves_cap;
     uint8_t *base = (sub < VECS ? c.k : c.v) + head * c.head_bytes + (sub % VECS) * 16;
-    for (int j0 = part * TAKE; j0 < moves; j0 += parts * TAKE) {
-      int64_t to = -1, from = -1;
-      if (lane < TAKE && j0 + lane < moves) {
-        int dslot, sslot, doff, soff;
-        split_entry(c, __ldcg(holes + j0 + lane), dslot, doff);
-        split_entry(c, __ldcg(movers + j0 + lane), sslot, soff);
-        const int dst = c.table[b * c.table_stride + dslot];
-        const int src = c.table[b * c.table_stride + sslot];
-        // the pages of a sequence that is not skipped were checked when they were claimed
-        to = dst * c.page_bytes + doff * c.entry_bytes;
-        from = src * c.page_bytes + soff * c.entry_bytes;
-        const int64_t tw = track_at(c, dst, head, doff), fw = track_at(c, src, head, soff);
-        c.weight[tw] = __ldcg(c.weight + fw);
-        c.order[tw] = __ldcg(c.order + fw);
+    int j0 = part * TAKE;
+    int dst = -1, src = 0;                     // rows (page * page size + place) of the lane's move
+    auto read_places = [&](int j) {
+      const bool in = lane < TAKE && j + lane < moves;
+      dst = in ? __ldcg(holes + j + lane) : -1;
+      src = in ? __ldcg(movers + j + lane) : 0;
+    };
+    if (j0 < moves) read_places(j0);
+    while (j0 < moves) {
+      int64_t to = -1, from = 0, tw = 0;
+      float weight = 0.f;
+      int32_t order = 0;
+      const bool mine = dst >= 0;
+      if (mine) {
+        int dpage, spage, doff, soff;
+        split_entry(c, dst, dpage, doff);
+        split_entry(c, src, spage, soff);
+        to = dpage * c.page_bytes + doff * c.entry_bytes;
+        from = spage * c.page_bytes + soff * c.entry_bytes;
+        const int64_t fw = track_at(c, spage, head, soff);
+        tw = track_at(c, dpage, head, doff);
+        weight = __ldcg(c.weight + fw);
+        order = __ldcg(c.order + fw);
       }
+      const int count = min(TAKE, moves - j0);
       uint4 row[kFlight];
-      int64_t dst[kFlight];
 #pragma unroll
       for (int i = 0; i < kFlight; ++i) {
         const int64_t s = __shfl_sync(0xffffffffu, from, i * PER + which);
-        dst[i] = __shfl_sync(0xffffffffu, to, i * PER + which);
-        if (dst[i] >= 0) row[i] = ld_stream(base + s);
+        if (i * PER + which < count) row[i] = ld_stream(base + s);
       }
+      j0 += parts * TAKE;
+      if (j0 < moves) read_places(j0);
 #pragma unroll
-      for (int i = 0; i < kFlight; ++i)
-        if (dst[i] >= 0) *reinterpret_cast<uint4 *>(base + dst[i]) = row[i];
+      for (int i = 0; i < kFlight; ++i) {
+        const int64_t d = __shfl_sync(0xffffffffu, to, i * PER + which);
+        if (i * PER + which < count) *reinterpret_cast<uint4 *>(base + d) = row[i];
+      }
+      if (mine) {
+        c.weight[tw] = weight;
+        c.order[tw] = order;
+      }
     }
   }
 }
@@ -355,15 +460,23 @@ __global__ void __launch_bounds__(kMoveWarps * 32)
 cudaError_t launch_evict(const EvictParams &p, int num_sms, cudaStream_t stream) {
   const CacheView &c = p.c;
   const int items = c.batch * c.hkv;
-  // CTAs per cluster and keys per thread by what the table can hold: one CTA up to 4096 entries, up
-  // to eight of them for longer ones
+  // One block where there are blocks enough or little to share, else up to eight that share the work of one:
+  // as long as all of them find a place (two per SM) and a share is more than 1024 entries.
   int ranks = 1;
-  while (ranks < 8 && c.cap > ranks * 4096) ranks *= 2;
-  const int share = (c.cap + ranks * kSelThreads - 1) / (ranks * kSelThreads);
-  auto kern = share <= 4 ? evict_select_kernel<4>
-                         : (share <= 8 ? evict_select_kernel<8> : evict_select_kernel<32>);
-  cudaError_t e = launch_dependent(kern, dim3(static_cast<unsigned>(items) * ranks), kSelThreads, 0,
-                                   ranks, stream, p);
+  while (ranks < 8 && (c.cap > ranks * kKeyRoom ||
+                       (c.cap > ranks * 1024 && items * ranks * 2 <= num_sms * 2)))
+    ranks *= 2;
+  // keys per CTA, in whole rows of 32 for each warp
+  const int64_t share = (static_cast<int64_t>(c.cap) + ranks - 1) / ranks;
+  const int room = static_cast<int>(
+      std::min<int64_t>(kKeyRoom, (share + kSelThreads - 1) / kSelThreads * kSelThreads));
+  static std::atomic<uint64_t> allowed[2];
+  const auto kern = ranks > 1 ? evict_select_kernel<kSelThreads, true>
+                              : evict_select_kernel<kSelThreads, false>;
+  cudaError_t e = allow_shared(kern, kKeyRoom * 4, &allowed[ranks > 1]);
+  if (e == cudaSuccess)
+    e = launch_dependent(kern, dim3(static_cast<unsigned>(items) * ranks), kSelThreads, room * 4, ranks,
+                         stream, p, room);
   if (e != cudaSuccess) return e;
   const int warps = num_sms * 4 * kMoveWarps;
   const int parts = std::max(1, warps / items);

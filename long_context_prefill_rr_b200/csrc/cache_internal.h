@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "rra_cache.h"
 
 namespace rra {
@@ -22,7 +24,8 @@ constexpr int decode_ctas(int head_dim) { return head_dim == 128 ? 2 : 3; }
 // The cache as the kernels see it.
 struct CacheView {
   int batch, hq, hkv, g, d;
-  int ps, ps_shift;            // page size, and its logarithm if it is a power of two, else -1
+  int ps;                      // page size
+  uint32_t ps_magic, ps_shift; // e / ps = (2 e * ps_magic >> 32) >> ps_shift for 0 <= e < 2^31
   int num_pages, max_pages, cap;   // cap = max_pages * ps
   int64_t page_bytes, head_bytes, entry_bytes;
   int64_t table_stride;
@@ -94,6 +97,20 @@ struct EvictParams {
   int32_t *moves;
   int64_t moves_cap;
 };
+
+// Allows a kernel more than 48 KB of shared memory, once per device (`allowed`: a bit for each).
+template <class... Params>
+cudaError_t allow_shared(void (*kern)(Params...), size_t bytes, std::atomic<uint64_t> *allowed) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
+  if (allowed->load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(bytes));
+  if (e == cudaSuccess) allowed->fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 // Launches a kernel that begins with griddepcontrol.wait: its blocks may be set up while the kernel before
 // it on the stream drains. cluster: blocks per cluster.

@@ -30,8 +30,6 @@
 // against 88).
 #include <math.h>
 
-#include <atomic>
-
 #include "cache_device.cuh"
 
 namespace rra {
@@ -509,18 +507,9 @@ __global__ void __launch_bounds__(kWeightThreads)
 
 template <class T, int D>
 cudaError_t launch_decode_t(const DecodeParams &p, cudaStream_t stream) {
-  // more than 48 KB of shared memory has to be allowed once per device
   static std::atomic<uint64_t> allowed{0};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  const cudaError_t e = allow_shared(paged_decode_kernel<T, D>, kRingBytes<D>, &allowed);
   if (e != cudaSuccess) return e;
-  const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
-  if ((allowed.load(std::memory_order_relaxed) & bit) == 0) {
-    e = cudaFuncSetAttribute(paged_decode_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(kRingBytes<D>));
-    if (e != cudaSuccess) return e;
-    allowed.fetch_or(bit, std::memory_order_relaxed);
-  }
   return launch_dependent(paged_decode_kernel<T, D>, dim3(p.grid), kThreads, kRingBytes<D>, 1, stream,
                           p);
 }

@@ -90,6 +90,8 @@ rra_status resolve_sizes(const rra_cache *s, CacheView *c) {
   if (s->head_dim != 64 && s->head_dim != 128) return RRA_ERR_UNSUPPORTED;
   const int64_t cap = static_cast<int64_t>(s->max_pages) * s->page_size;
   if (cap > (1 << 30)) return RRA_ERR_UNSUPPORTED;
+  // rows of the cache (page * page_size + place) are counted in 31 bits
+  if (static_cast<int64_t>(s->num_pages) * s->page_size > INT_MAX) return RRA_ERR_UNSUPPORTED;
   const int g = s->heads_q / s->heads_kv;
   // units of work, table places and heads are counted in 32 bits
   const int64_t tiles = (g + rra::kDecodeHeads - 1) / rra::kDecodeHeads;
@@ -105,10 +107,12 @@ rra_status resolve_sizes(const rra_cache *s, CacheView *c) {
   c->g = g;
   c->d = s->head_dim;
   c->ps = s->page_size;
-  c->ps_shift = -1;
-  if ((s->page_size & (s->page_size - 1)) == 0)
-    for (c->ps_shift = 0; (1 << c->ps_shift) < s->page_size; ++c->ps_shift) {
-    }
+  // ps_magic = ceil(2^(31 + k) / ps) with 2^k >= ps: it exceeds the quotient by less than 2^k / ps, so
+  // e * ps_magic / 2^(31 + k) exceeds e / ps by less than e / (2^31 ps), too little to reach the next
+  // integer while e < 2^31; and ps_magic < 2^32
+  while ((int64_t{1} << c->ps_shift) < s->page_size) ++c->ps_shift;
+  c->ps_magic = static_cast<uint32_t>(((uint64_t{1} << (31 + c->ps_shift)) + s->page_size - 1) /
+                                      s->page_size);
   c->num_pages = s->num_pages;
   c->max_pages = s->max_pages;
   c->cap = static_cast<int>(cap);

@@ -530,13 +530,15 @@ def weights(p, kind, seed=0):
         w.fill_(0.5)
     elif kind == "zero":
         w.zero_()
+    elif kind == "tiny":                    # the smallest weights: multiples of 2^-149, zeros among them
+        w = torch.floor(r * 40 - 8).clamp(min=0).to(torch.int32).view(torch.float32)
     elif kind == "odd":
         for i, x in enumerate((math.nan, -1.0, math.inf, -0.0, 1e-42, -math.inf)):
             w[(r > i * 0.1) & (r < i * 0.1 + 0.1)] = x
     return w
 
 
-@pytest.mark.parametrize("kind", ["plain", "ties", "equal", "zero", "odd"])
+@pytest.mark.parametrize("kind", ["plain", "ties", "equal", "zero", "odd", "tiny"])
 @pytest.mark.parametrize("lens,budget,sinks,recent,ps,hkv,d", [
     ([1, 0, 2, 3], 1, 0, 1, 1, 2, 64), ([64, 65, 66, 200], 64, 4, 20, 16, 3, 128),
     ([500, 31, 32, 33], 32, 0, 0, 7, 2, 64), ([1500, 1499], 1499, 100, 1399, 20, 1, 128),
