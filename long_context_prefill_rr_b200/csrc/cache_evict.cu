@@ -30,7 +30,6 @@ namespace {
 constexpr int kBins = 256;
 constexpr int kPasses = 4;         // digits of 8, 8, 8 and 7 bits from bit 30 down
 constexpr uint32_t kProtected = 0x7fffffffu;
-constexpr int kSelThreads = 512;
 constexpr int kKeyRoom = 16384;    // keys that a CTA of a cluster holds in shared memory, 64 KB
 constexpr int kMoveWarps = 8;
 
@@ -176,28 +175,30 @@ __device__ __noinline__ int load_keys(const EvictParams &p, int b, int head, int
   int safe = 0;
   const int lane = threadIdx.x & 31;
   const int32_t *table = c.table + b * c.table_stride;
+  int page[BATCH], off[BATCH];
+  auto look_up = [&](int i) {
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      if (i + k >= count) break;
+      int slot;
+      split_entry(c, min(e0 + (i + k) * 32 + lane, end - 1), slot, off[k]);
+      page[k] = table[slot];
+    }
+  };
+  if (count > 0) look_up(0);
 #pragma unroll 1
   for (int i = 0; i < count; i += BATCH) {
-    int page[BATCH];
     int32_t order[BATCH];
     float w[BATCH];
 #pragma unroll
     for (int k = 0; k < BATCH; ++k) {
       if (i + k >= count) break;
-      int slot, off;
-      split_entry(c, min(e0 + (i + k) * 32 + lane, end - 1), slot, off);
-      page[k] = table[slot];
-    }
-#pragma unroll
-    for (int k = 0; k < BATCH; ++k) {
-      if (i + k >= count) break;
-      int slot, off;
-      split_entry(c, min(e0 + (i + k) * 32 + lane, end - 1), slot, off);
       const int pg = static_cast<unsigned>(page[k]) < static_cast<unsigned>(c.num_pages) ? page[k] : 0;
-      const int64_t at = track_at(c, pg, head, off);
+      const int64_t at = track_at(c, pg, head, off[k]);
       order[k] = __ldcg(c.order + at);
       w[k] = __ldcg(c.weight + at);
     }
+    look_up(i + BATCH);          // the next pages, while the weights are on their way
 #pragma unroll
     for (int k = 0; k < BATCH; ++k) {
       if (i + k >= count) break;
@@ -214,7 +215,7 @@ __device__ __noinline__ int load_keys(const EvictParams &p, int b, int head, int
 // memory holds; a CTA's share of more entries is taken in rounds and read again for every digit. Loops are
 // kept rolled: a short call is bound by latencies, instruction fetches among them.
 template <int THREADS, bool CLUSTER>
-__global__ void __launch_bounds__(THREADS, 2)
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     evict_select_kernel(const __grid_constant__ EvictParams p, int room) {
   constexpr int WARPS = THREADS / 32;
   extern __shared__ uint32_t s_keys[];
@@ -343,6 +344,7 @@ __global__ void __launch_bounds__(THREADS, 2)
     int2 seen = make_int2(0, 0);
     for (int round = 0; round < rounds; ++round) {
       const int rows = rows_of(round, false), e0 = wlo + round * take * 32;
+#pragma unroll 4
       for (int i = 0; i < rows; ++i) {
         const uint2 m = masks(e0, i);
         seen.x += __popc(m.x);
@@ -355,21 +357,30 @@ __global__ void __launch_bounds__(THREADS, 2)
     rank_now = tie_rank;
     for (int round = 0; round < rounds; ++round) {
       const int rows = rows_of(round, false), e0 = wlo + round * take * 32;
-      for (int i = 0; i < rows; ++i) {
-        const uint2 m = rounds == 1 ? make_uint2(keys[i * 32], keys[i * 32 + 1]) : masks(e0, i);
-        if ((m.x | m.y) == 0) continue;
-        if (((m.x | m.y) >> lane) & 1u) {
-          int slot, off;
-          split_entry(c, e0 + i * 32 + lane, slot, off);
-          // (page, place) as one number; a sequence with a bad page is left alone
-          const int row = c.table[b * c.table_stride + slot] * c.ps + off;
-          if ((m.x >> lane) & 1u)
-            holes[to.x + __popc(m.x & below)] = row;
-          else
-            movers[to.y + __popc(m.y & below)] = row;
+      constexpr int BATCH = 4;
+      for (int i0 = 0; i0 < rows; i0 += BATCH) {
+        uint2 m[BATCH];
+        int row[BATCH];
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) {
+          const int i = i0 + k;
+          m[k] = make_uint2(0, 0);
+          if (i < rows) m[k] = rounds == 1 ? make_uint2(keys[i * 32], keys[i * 32 + 1]) : masks(e0, i);
+          row[k] = -1;
+          if (((m[k].x | m[k].y) >> lane) & 1u) {
+            // (page, place) as one number; a sequence with a bad page is left alone
+            int slot, off;
+            split_entry(c, e0 + i * 32 + lane, slot, off);
+            row[k] = c.table[b * c.table_stride + slot] * c.ps + off;
+          }
         }
-        to.x += __popc(m.x);
-        to.y += __popc(m.y);
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) {
+          if ((m[k].x >> lane) & 1u) holes[to.x + __popc(m[k].x & below)] = row[k];
+          if ((m[k].y >> lane) & 1u) movers[to.y + __popc(m[k].y & below)] = row[k];
+          to.x += __popc(m[k].x);
+          to.y += __popc(m[k].y);
+        }
       }
     }
   }
@@ -384,7 +395,7 @@ __global__ void __launch_bounds__(THREADS, 2)
 constexpr int kFlight = 8;
 
 template <int D>
-__global__ void __launch_bounds__(kMoveWarps * 32, 4)
+__global__ void __launch_bounds__(kMoveWarps * 32, 3)
     evict_move_kernel(const __grid_constant__ EvictParams p, int parts) {
   constexpr int VECS = D / 8;                  // 16-byte vectors of a row
   constexpr int PER = 32 / (2 * VECS);         // moves whose key and value rows fill a warp: 1 or 2
@@ -460,28 +471,34 @@ __global__ void __launch_bounds__(kMoveWarps * 32, 4)
 cudaError_t launch_evict(const EvictParams &p, int num_sms, cudaStream_t stream) {
   const CacheView &c = p.c;
   const int items = c.batch * c.hkv;
-  // One block where there are blocks enough or little to share, else up to eight that share the work of one:
-  // as long as all of them find a place (two per SM) and a share is more than 1024 entries.
+  // One block where there are blocks enough or little to share, else up to eight that share the work of one,
+  // as long as all of them find an SM and a share is more than 1024 entries. Long shares take the
+  // largest blocks: two smaller ones would be put on one SM while others idle.
   int ranks = 1;
-  while (ranks < 8 && (c.cap > ranks * kKeyRoom ||
-                       (c.cap > ranks * 1024 && items * ranks * 2 <= num_sms * 2)))
+  while (ranks < 8 &&
+         (c.cap > ranks * kKeyRoom || (c.cap > ranks * 1024 && items * ranks * 2 <= num_sms)))
     ranks *= 2;
+  const int threads = c.cap > ranks * 4096 ? 1024 : 512;
   // keys per CTA, in whole rows of 32 for each warp
   const int64_t share = (static_cast<int64_t>(c.cap) + ranks - 1) / ranks;
-  const int room = static_cast<int>(
-      std::min<int64_t>(kKeyRoom, (share + kSelThreads - 1) / kSelThreads * kSelThreads));
-  static std::atomic<uint64_t> allowed[2];
-  const auto kern = ranks > 1 ? evict_select_kernel<kSelThreads, true>
-                              : evict_select_kernel<kSelThreads, false>;
-  cudaError_t e = allow_shared(kern, kKeyRoom * 4, &allowed[ranks > 1]);
+  const int room =
+      static_cast<int>(std::min<int64_t>(kKeyRoom, (share + threads - 1) / threads * threads));
+  static std::atomic<uint64_t> allowed[4];
+  const auto kern =
+      ranks > 1 ? (threads == 1024 ? evict_select_kernel<1024, true> : evict_select_kernel<512, true>)
+                : (threads == 1024 ? evict_select_kernel<1024, false> : evict_select_kernel<512, false>);
+  cudaError_t e = allow_shared(kern, kKeyRoom * 4, &allowed[(ranks > 1) * 2 + threads / 1024]);
   if (e == cudaSuccess)
-    e = launch_dependent(kern, dim3(static_cast<unsigned>(items) * ranks), kSelThreads, room * 4, ranks,
+    e = launch_dependent(kern, dim3(static_cast<unsigned>(items) * ranks), threads, room * 4, ranks,
                          stream, p, room);
   if (e != cudaSuccess) return e;
-  const int warps = num_sms * 4 * kMoveWarps;
-  const int parts = std::max(1, warps / items);
-  const int64_t blocks = (static_cast<int64_t>(items) * parts + kMoveWarps - 1) / kMoveWarps;
-  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(num_sms * 4, blocks)));
+  // Blocks of the move kernel: as many as its longest possible lists can use, up to twelve per SM, so that
+  // the hardware evens out items with many moves and with none.
+  const int64_t most = std::max(1, std::min(p.budget, c.cap - p.budget));
+  const int per_block = kMoveWarps * kFlight * (c.d == 128 ? 1 : 2);
+  const int64_t blocks = std::min<int64_t>(num_sms * 12, items * ((most + per_block - 1) / per_block));
+  const dim3 grid(static_cast<unsigned>(blocks));
+  const int parts = static_cast<int>(std::max<int64_t>(1, blocks * kMoveWarps / items));
   return c.d == 128 ? launch_dependent(evict_move_kernel<128>, grid, kMoveWarps * 32, 0, 1, stream,
                                        p, parts)
                     : launch_dependent(evict_move_kernel<64>, grid, kMoveWarps * 32, 0, 1, stream,
