@@ -3,8 +3,9 @@
 // Pair i of a head turns by phi = position[axis(i)] * f_i: (x, y) -> (x cos - y sin, y cos + x sin);
 // the gradient turns back (sin negated). f_i is kept as F_i = f_i / (2 pi) * 2^64, an integer, so
 // position * F_i mod 2^64 is the fraction of a turn with the full turns dropped, exact to 2^-64 *
-// position; its top 32 bits, as a signed number, go to sincospif. An fp32 product
-// position * f_i would be off by 2^-24 * position radians, 0.06 at a million.
+// position. (An fp32 product position * f_i would be off by 2^-24 * position radians, 0.06 at a million.)
+// Its top two bits, rounded, are the quadrant; sine and cosine of the rest, at most an eighth of a turn,
+// come from their Taylor series.
 //
 // Memory bound: every row is read once and written once (twice where the prefill's copy and the
 // cache both want it). A thread owns one unit of 16 dimensions (two 16-byte vectors: for halves one
@@ -13,6 +14,8 @@
 #include "cache_device.cuh"
 
 namespace rra {
+
+constexpr int kBlocks = 5;   // blocks that share an SM
 
 struct RopeUnit {
   float c[8], s[8];
@@ -41,8 +44,60 @@ __device__ __forceinline__ void turn(const RopeUnit &r, uint4 &a, uint4 &b) {
   }
 }
 
+// Top 32 bits of position * turn mod 2^64.
+__device__ __forceinline__ uint32_t fraction(int32_t position, uint64_t turn) {
+  const uint32_t lo = static_cast<uint32_t>(turn), hi = static_cast<uint32_t>(turn >> 32);
+  const uint32_t x = static_cast<uint32_t>(position);
+  return __umulhi(x, lo) + x * hi - (position < 0 ? lo : 0u);
+}
+
+// Cosine and sine of f / 2^32 turns. With |x| <= pi / 4 the series are cut below 2^-25 (x^11 / 11!, x^10 / 10!).
+__device__ __forceinline__ void cos_sin(uint32_t f, float &c, float &s) {
+  const uint32_t quadrant = (f + 0x20000000u) >> 30;
+  const float x = static_cast<float>(static_cast<int32_t>(f - (quadrant << 30))) * 1.4629180792671596e-9f;
+  const float xx = x * x;
+  float sine = fmaf(xx, 1.f / 362880.f, -1.f / 5040.f);
+  sine = fmaf(xx, sine, 1.f / 120.f);
+  sine = fmaf(xx, sine, -1.f / 6.f);
+  sine = fmaf(x * xx, sine, x);
+  float cosine = fmaf(xx, 1.f / 40320.f, -1.f / 720.f);
+  cosine = fmaf(xx, cosine, 1.f / 24.f);
+  cosine = fmaf(xx, cosine, -0.5f);
+  cosine = fmaf(xx, cosine, 1.f);
+  // a quarter turn takes (cos, sin) to (-sin, cos)
+  const float a = (quadrant & 1u) ? sine : cosine, b = (quadrant & 1u) ? cosine : sine;
+  c = __uint_as_float(__float_as_uint(a) ^ (((quadrant + 1u) & 2u) << 30));
+  s = __uint_as_float(__float_as_uint(b) ^ ((quadrant & 2u) << 30));
+}
+
+// Heads h0 .. h1 - 1 of one tensor: from `in` to `out` and to `page`, where those are given (byte offsets
+// of the two vectors: a and b).
+template <class T, bool ADJACENT, bool TURN>
+__device__ __forceinline__ void heads(const RopeUnit &r, int h0, int h1, int a, int b,
+                                      const uint8_t *in, int64_t in_head, uint8_t *out,
+                                      int64_t out_head, uint8_t *page, int64_t page_head) {
+  in += h0 * in_head;
+  out += h0 * out_head;
+  page += h0 * page_head;
+  const bool to_out = out_head >= 0, to_page = page_head >= 0;
+#pragma unroll 1
+  for (int h = h0; h < h1; ++h, in += in_head, out += out_head, page += page_head) {
+    uint4 x = *reinterpret_cast<const uint4 *>(in + a);
+    uint4 y = *reinterpret_cast<const uint4 *>(in + b);
+    if (TURN) rra::turn<T, ADJACENT>(r, x, y);
+    if (to_out) {
+      *reinterpret_cast<uint4 *>(out + a) = x;
+      *reinterpret_cast<uint4 *>(out + b) = y;
+    }
+    if (to_page) {
+      *reinterpret_cast<uint4 *>(page + a) = x;
+      *reinterpret_cast<uint4 *>(page + b) = y;
+    }
+  }
+}
+
 template <class T, bool ADJACENT, bool CACHED>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, kBlocks)
     rope_kernel(const __grid_constant__ RopeParams p, const __grid_constant__ CacheView c) {
   grid_dependency_wait();
   grid_dependents_go();
@@ -52,76 +107,77 @@ __global__ void __launch_bounds__(256)
   const int u = static_cast<int>(idx - row * units);
   const int b = static_cast<int>(row / p.tokens);
   const int t = static_cast<int>(row - static_cast<int64_t>(b) * p.tokens);
-  bool real = b < p.batch;
-  if (real && p.new_len) real = t < p.new_len[b];
-  int page = -1, off = 0, ordinal = 0;
-  if (CACHED && real) {
-    const int e = cache_len(c, b) + t;
-    if (e < c.cap) {
-      int slot;
-      split_entry(c, e, slot, off);
-      page = page_at(c, b, slot);
-      if (c.order) ordinal = c.seen[b] + t;
+  // everything that the token's rows do not depend on is asked for at once
+  const bool there = b < p.batch;
+  const bool turned = u < p.rot / 16;
+  int32_t pos[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  int first = 0, new_tokens = p.tokens, ordinal = 0;
+  if (there) {
+    if (p.new_len) new_tokens = p.new_len[b];
+    if (CACHED) first = c.len[b];
+    if (CACHED && c.order) ordinal = c.seen[b] + t;
+    if (turned) {
+      const int32_t *at = p.pos.data + b * p.pos.batch + t * p.pos.token;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) pos[i] = at[p.axis[u * 8 + i] * p.pos.axis];
     }
   }
+  const bool real = there && t < new_tokens;
   if (real) {
-    const bool turned = u < p.rot / 16;
-    const int a0 = (!ADJACENT && turned) ? u * 16 : u * 32;             // byte offsets in a row
-    const int b0 = (!ADJACENT && turned) ? p.rot + u * 16 : u * 32 + 16;
+    int page = -1, off = 0;
+    if (CACHED) {
+      const int e = max(0, min(first, c.cap)) + t;
+      int slot;
+      split_entry(c, e, slot, off);
+      if (e < c.cap) page = c.table[b * c.table_stride + slot];
+    }
+    const int va = (!ADJACENT && turned) ? u * 16 : u * 32;             // byte offsets in a row
+    const int vb = (!ADJACENT && turned) ? p.rot + u * 16 : u * 32 + 16;
     RopeUnit r;
     if (turned) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int pair = u * 8 + i;
-        const int64_t pos = p.pos.data[p.axis[pair] * p.pos.axis + b * p.pos.batch +
-                                       t * p.pos.token];
-        const uint64_t frac = static_cast<uint64_t>(pos) * p.turn[pair];
-        const float half_turns = static_cast<float>(static_cast<int32_t>(frac >> 32)) * 0x1p-31f;
-        sincospif(half_turns, &r.s[i], &r.c[i]);
+        cos_sin(fraction(pos[i], p.turn[u * 8 + i]), r.c[i], r.s[i]);
         if (p.inverse) r.s[i] = -r.s[i];
       }
     }
-    const int h0 = blockIdx.y * p.heads_per_thread;
-    const int h1 = min(h0 + p.heads_per_thread, p.heads);
-    const int nq = p.q.data ? p.hq : 0;
-    const int nk = p.k.data ? p.hkv : 0;
-#pragma unroll 4
-    for (int h = h0; h < h1; ++h) {
-      const bool is_q = h < nq, is_v = h >= nq + nk;
-      const rra_view &src = is_q ? p.q : (is_v ? p.v : p.k);
-      const rra_view &dst = is_q ? p.qo : (is_v ? p.vo : p.ko);
-      const int hh = is_q ? h : (is_v ? h - nq - nk : h - nq);
-      const uint8_t *in = static_cast<const uint8_t *>(src.data) + b * src.batch +
-                          hh * src.head + t * src.token;
-      uint4 x = *reinterpret_cast<const uint4 *>(in + a0);
-      uint4 y = *reinterpret_cast<const uint4 *>(in + b0);
-      if (turned && !is_v) rra::turn<T, ADJACENT>(r, x, y);
-      if (dst.data) {
-        uint8_t *o = static_cast<uint8_t *>(dst.data) + b * dst.batch + hh * dst.head +
-                     t * dst.token;
-        *reinterpret_cast<uint4 *>(o + a0) = x;
-        *reinterpret_cast<uint4 *>(o + b0) = y;
-      }
-      if (CACHED && !is_q && page >= 0) {
-        uint8_t *o = (is_v ? c.v : c.k) + page * c.page_bytes + hh * c.head_bytes +
-                     off * c.entry_bytes;
-        *reinterpret_cast<uint4 *>(o + a0) = x;
-        *reinterpret_cast<uint4 *>(o + b0) = y;
-        if (c.order && is_v && u == 0) {
-          const int64_t at = track_at(c, page, hh, off);
-          c.weight[at] = 0.f;
-          c.order[at] = ordinal;
-        }
-      }
+    if (CACHED && static_cast<unsigned>(page) >= static_cast<unsigned>(c.num_pages)) {
+      if (max(0, min(first, c.cap)) + t < c.cap) raise(c.status, kErrBadPage);
+      page = -1;
     }
+    // the heads of q, then of k, then of v are shared out over blockIdx.y
+    const int h0 = blockIdx.y * p.heads_per_thread, h1 = h0 + p.heads_per_thread;
+    auto part = [&](const rra_view &src, const rra_view &dst, int first, int count, uint8_t *cache,
+                    bool turn_it) {
+      if (!src.data) return;
+      const int lo = max(h0 - first, 0), hi = min(h1 - first, count);
+      if (lo >= hi) return;
+      const uint8_t *in = static_cast<const uint8_t *>(src.data) + b * src.batch + t * src.token;
+      uint8_t *out = static_cast<uint8_t *>(dst.data) + b * dst.batch + t * dst.token;
+      const bool paged = CACHED && cache != nullptr && page >= 0;
+      uint8_t *to = paged ? cache + page * c.page_bytes + off * c.entry_bytes : nullptr;
+      const int64_t out_head = dst.data ? dst.head : -1, to_head = paged ? c.head_bytes : -1;
+      if (turn_it)
+        heads<T, ADJACENT, true>(r, lo, hi, va, vb, in, src.head, out, out_head, to, to_head);
+      else
+        heads<T, ADJACENT, false>(r, lo, hi, va, vb, in, src.head, out, out_head, to, to_head);
+    };
+    const int nq = p.q.data ? p.hq : 0, nk = p.k.data ? p.hkv : 0;
+    part(p.q, p.qo, 0, nq, nullptr, turned);
+    part(p.k, p.ko, nq, nk, c.k, turned);
+    part(p.v, p.vo, nq + nk, p.v.data ? p.hkv : 0, c.v, false);
+    if (CACHED && c.order && page >= 0 && u == 0)
+      for (int h = max(h0 - nq - nk, 0); h < min(h1 - nq - nk, p.hkv); ++h) {
+        const int64_t at = track_at(c, page, h, off);
+        c.weight[at] = 0.f;
+        c.order[at] = ordinal;
+      }
   }
   if (!CACHED) return;
   // lengths outside the table, reported once per sequence
-  if (blockIdx.y == 0 && real && t == 0 && u == 0) {
-    const int n = c.len[b];
-    const int add = p.new_len ? min(p.new_len[b], p.tokens) : p.tokens;
-    if (n < 0 || static_cast<int64_t>(n) + add > c.cap) raise(c.status, kErrBadLength);
-  }
+  if (blockIdx.y == 0 && real && t == 0 && u == 0 &&
+      (first < 0 || static_cast<int64_t>(first) + min(new_tokens, p.tokens) > c.cap))
+    raise(c.status, kErrBadLength);
   if (!p.advance) return;
   // The last block to have read len and seen moves them on and resets the count.
   __shared__ uint32_t s_last;
@@ -156,9 +212,10 @@ cudaError_t launch_rope(const RopeParams &in, const CacheView *cache, int dtype,
   RopeParams p = in;
   const int64_t threads = static_cast<int64_t>(p.batch) * p.tokens * (p.d / 16);
   const int64_t blocks = (threads + 255) / 256;
-  // heads are shared out over blockIdx.y until every SM has its fill of threads
-  const int64_t want = (static_cast<int64_t>(num_sms) * 8 + blocks - 1) / blocks;
-  const int split = static_cast<int>(want < 1 ? 1 : (want > p.heads ? p.heads : want));
+  // Heads are shared out over blockIdx.y as long as all blocks find a place at once: a second,
+  // partly filled round costs more than longer blocks.
+  const int64_t fit = static_cast<int64_t>(num_sms) * kBlocks / blocks;
+  const int split = static_cast<int>(fit < 1 ? 1 : (fit > p.heads ? p.heads : fit));
   p.heads_per_thread = (p.heads + split - 1) / split;
   const dim3 grid(static_cast<unsigned>(blocks),
                   static_cast<unsigned>((p.heads + p.heads_per_thread - 1) / p.heads_per_thread));
