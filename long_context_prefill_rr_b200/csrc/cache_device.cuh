@@ -19,6 +19,12 @@ __device__ __forceinline__ void grid_dependents_go() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+__device__ __forceinline__ int atomic_add_acq_rel(int32_t *p, int x) {
+  int old;
+  asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(x) : "memory");
+  return old;
+}
+
 __device__ __forceinline__ void raise(uint32_t *status, uint32_t bit) { atomicOr(status, bit); }
 
 // Length of sequence b, clamped to what the page table can hold.

@@ -89,14 +89,26 @@ __device__ int locate(const CacheView &c, int items, int grid, int cta, int *s_s
                       int *total_out) {
   const int tid = threadIdx.x, nt = blockDim.x;
   const int lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
-  if (c.batch == 1) {
-    const int len = cache_len(c, 0);
-    cur->b = 0;
-    cur->start = 0;
-    cur->units = units_of(len);
-    cur->len = len;
-    *total_out = cur->units * items;
-    return max(1, (*total_out + grid - 1) / grid);
+  if (c.batch <= 32) {
+    // a lane per sequence, and every warp for itself
+    const int len = lane < c.batch ? cache_len(c, lane) : 0;
+    const int mine = units_of(len) * items;
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    const int total = __shfl_sync(0xffffffffu, incl, 31);
+    const int per = max(1, (total + grid - 1) / grid);
+    const uint32_t past = __ballot_sync(0xffffffffu, incl > per * cta);
+    const int b = past ? __ffs(past) - 1 : 0;
+    cur->b = b;
+    cur->start = __shfl_sync(0xffffffffu, incl - mine, b);
+    cur->len = __shfl_sync(0xffffffffu, len, b);
+    cur->units = units_of(cur->len);
+    *total_out = total;
+    return per;
   }
   const int chunk = (c.batch + nt - 1) / nt;
   const int b0 = min(tid * chunk, c.batch), b1 = min(b0 + chunk, c.batch);
@@ -250,25 +262,27 @@ __global__ void __launch_bounds__(kThreads, decode_ctas(D))
       return __ballot_sync(0xffffffffu, at >= 0) & 0xffffu;
     };
 
-    int kb = unit0 * kDecodeUnit + warp * 16;
-    int ahead = kb;                    // first entry of the next fetch
-    uint64_t exist = 0;                // 16 bits per stage in flight, the oldest lowest
+    // Step i is fetched into stage i mod S and used S - 1 steps later.
+    int kb = unit0 * kDecodeUnit + (warp - (S - 1) * kWarps) * 16;   // entries that are used
+    int ahead = unit0 * kDecodeUnit + warp * 16;                     // entries that are fetched
+    uint64_t exist = 0;                // 16 bits per stage in flight, the newest on top
     int64_t at = place(ahead);
-#pragma unroll
-    for (int st = 0; st < S; ++st) {
-      const int64_t now = at;
-      const bool more = ahead < key1;
-      ahead += kDecodeUnit;
-      at = place(ahead);
-      if (more) exist |= static_cast<uint64_t>(fetch(st, now)) << (16 * st);
+    for (int in = 0, st = 1 % S; kb < key1; kb += kDecodeUnit) {
+      exist >>= 16;
+      if (ahead < key1) {
+        exist |= static_cast<uint64_t>(fetch(in, at)) << (16 * (S - 1));
+        ahead += kDecodeUnit;
+        at = place(ahead);
+      }
       copy_commit();
-    }
-    int st = 0;
-    for (; kb < key1; kb += kDecodeUnit) {
+      in = in + 1 == S ? 0 : in + 1;
+      const int now = st;
+      st = st + 1 == S ? 0 : st + 1;
+      if (kb < unit0 * kDecodeUnit) continue;
       copy_wait<S - 1>();
       __syncwarp();                    // the other lanes' copies of the stage have landed too
-      const uint32_t kst = ring + st * STAGE + t * 16;
-      const uint32_t vst = ring + st * STAGE + 16 * PITCH + r * 16;
+      const uint32_t kst = ring + now * STAGE + t * 16;
+      const uint32_t vst = ring + now * STAGE + 16 * PITCH + r * 16;
       // logits of head r for columns 2t, 2t + 1 of the first MMA tile and of the second
       float s[2][4];
 #pragma unroll
@@ -307,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, decode_ctas(D))
       float w[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        w[i] = exp2f(x[i] - base);
+        w[i] = fast_exp2(x[i] - base);
         l_run += w[i];
       }
       const uint32_t hi0 = Elem<T>::pack(w[0], w[1]), hi1 = Elem<T>::pack(w[2], w[3]);
@@ -332,16 +346,7 @@ __global__ void __launch_bounds__(kThreads, decode_ctas(D))
                        __byte_perm(v2[e >> 1], v3[e >> 1], pick));
         }
       }
-      // every lane's reads of the stage fed the MMAs above, so its rows can be filled again
-      __syncwarp();
-      exist >>= 16;
-      if (ahead < key1) {
-        exist |= static_cast<uint64_t>(fetch(st, at)) << (16 * (S - 1));
-        ahead += kDecodeUnit;
-        at = place(ahead);
-      }
-      copy_commit();
-      st = st + 1 == S ? 0 : st + 1;
+      __syncwarp();                    // every lane's reads fed the MMAs above: the stage is free
     }
     copy_wait<0>();
     __syncwarp();
@@ -408,16 +413,15 @@ __global__ void __launch_bounds__(kThreads, decode_ctas(D))
 
     if (!whole) {
       // ---- the last of the item's CTAs joins its pieces, in the order of the entries
-      __threadfence();
       __syncthreads();
       if (threadIdx.x == 0) {
-        const int done = atomicAdd(&p.counters[item], 1);
+        // releases the block's writes (which the barrier orders before it) and acquires the others'
+        const int done = atomic_add_acq_rel(&p.counters[item], 1);
         s_scan[19] = done == cta1 - cta0;
         if (done == cta1 - cta0) p.counters[item] = 0;
       }
       __syncthreads();
       if (s_scan[19]) {
-        __threadfence();
         for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads) {
           const int row = i / (D / 4), col = (i - row * (D / 4)) * 4;
           float mt = -INFINITY, l = 0.f;
