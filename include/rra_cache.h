@@ -83,7 +83,7 @@ typedef struct {
   int head_dim;          /* 64 or 128 */
   int dtype;             /* rra_dtype of k, v, queries and outputs */
   int page_size;         /* entries per page >= 1 */
-  int num_pages;         /* pages of k and v >= 1; num_pages * page_size < 2^31 */
+  int num_pages;         /* pages of k and v >= 1 */
   int max_pages;         /* page_table entries per sequence >= 1; max_pages * page_size <= 2^30 */
   float softmax_scale;   /* <= 0 means 1/sqrt(head_dim) */
   int reserved;          /* 0 */

@@ -16,6 +16,8 @@
 // short caches the chain of dependent steps (length, page, weight, three digits).
 #include <cooperative_groups.h>
 
+#include <limits.h>
+
 #include <algorithm>
 #include <atomic>
 
@@ -32,20 +34,13 @@ constexpr int kPasses = 4;         // digits of 8, 8, 8 and 7 bits from bit 30 d
 constexpr uint32_t kProtected = 0x7fffffffu;
 constexpr int kKeyRoom = 16384;    // keys that a CTA of a cluster holds in shared memory, 64 KB
 constexpr int kMoveWarps = 8;
-
-// Orders entries by what is kept first: protected entries, then the weight. Weights that are not
-// above zero are 0; positive floats order like their bits, infinity is 0x7f800000. 31 bits.
-__device__ __forceinline__ uint32_t entry_key(const EvictParams &p, int32_t order, float w,
-                                              int64_t recent_from) {
-  if (order < p.sinks || order >= recent_from) return kProtected;
-  return w > 0.f ? __float_as_uint(w) : 0u;
-}
+constexpr int kRanks = 8;          // CTAs of a cluster at most
 
 // What a sequence is cut by.
 struct Cut {
   int n;               // entries
   uint32_t tag;        // the call's mark, one above the count of calls (the move kernel moves that on)
-  int64_t recent_from; // ordinals from here on are protected
+  int recent_from;     // ordinals from here on are protected
 };
 
 __device__ __forceinline__ Cut read_cut(const EvictParams &p, int b, bool first) {
@@ -53,7 +48,9 @@ __device__ __forceinline__ Cut read_cut(const EvictParams &p, int b, bool first)
   const int raw = c.len[b];
   Cut cut;
   cut.tag = *p.epoch + 1u;
-  cut.recent_from = static_cast<int64_t>(c.seen[b]) - p.recent;
+  // seen - recent, or the lowest ordinal if that is below it
+  const int seen = c.seen[b];
+  cut.recent_from = seen < INT_MIN + p.recent ? INT_MIN : seen - p.recent;
   cut.n = raw < 0 ? 0 : min(raw, c.cap);
   if (first) {
     if (raw != cut.n) raise(c.status, kErrBadLength);
@@ -102,11 +99,11 @@ __device__ __forceinline__ int digit_shift(int pass) { return pass == 3 ? 0 : 23
 // What the descent has found: `prefix` holds the digits of the want-th largest key so far, `ties` the
 // keys that share them.
 struct Found {
-  uint32_t prefix, want, ties;
+  uint32_t prefix, want, ties, more;   // more: there is a next digit
 };
 
-// One digit. Every warp searches the bins for itself (lane i holds eight of them, from the top).
-// Returns false if the bins hold fewer than f->want keys, which are taken off f->want.
+// One digit, found by one warp (lane i holds eight of the bins, from the top). Returns false if the bins
+// hold fewer than f->want keys, which are taken off f->want.
 __device__ __forceinline__ bool descend(const uint32_t *bins, int pass, Found *f) {
   const int lane = threadIdx.x & 31;
   const int top = kBins - 8 - 8 * lane;
@@ -165,24 +162,34 @@ __device__ __forceinline__ int2 prefix_of_warps(int2 mine, int2 *s_warp, int2 *s
   return before;
 }
 
-// Keys of the entries e0 + 32 i + lane, i < count, to keys[32 i + lane]; entries at or past `end` get
-// key 0. The pages of a batch are looked up together, then its weights and ordinals; a page that is
-// none (the sequence is left alone) reads as page 0. Returns the protected entries of the warp.
-__device__ __noinline__ int load_keys(const EvictParams &p, int b, int head, int64_t recent_from,
-                                      int e0, int end, int count, uint32_t *keys) {
+// What the keys of a (sequence, KV head) are made of; passed by value, so that it stays in registers.
+struct KeySource {
+  const int32_t *table, *order;   // the sequence's pages; the head's ordinals and
+  const float *weight;            // weights in page 0
+  int page_stride, num_pages, ps;
+  uint32_t ps_magic, ps_shift;
+  int sinks, recent_from;
+};
+
+// Keys of the entries e0 + 32 i + lane, i < count, to keys[32 i + lane]: what is kept first has the larger
+// key. Protected entries come first, then the weight: those not above zero are 0, positive floats order
+// like their bits and infinity is 0x7f800000, so 31 bits do. Entries at or past `end` get key 0. The
+// pages of a batch are looked up together, then its weights and ordinals; a page that is none (the
+// sequence is left alone) reads as page 0. Returns the protected entries of the warp.
+__device__ __noinline__ int load_keys(const KeySource src, int e0, int end, int count, uint32_t *keys) {
   constexpr int BATCH = 4;
-  const CacheView &c = p.c;
   int safe = 0;
   const int lane = threadIdx.x & 31;
-  const int32_t *table = c.table + b * c.table_stride;
   int page[BATCH], off[BATCH];
   auto look_up = [&](int i) {
 #pragma unroll
     for (int k = 0; k < BATCH; ++k) {
       if (i + k >= count) break;
-      int slot;
-      split_entry(c, min(e0 + (i + k) * 32 + lane, end - 1), slot, off[k]);
-      page[k] = table[slot];
+      const int e = min(e0 + (i + k) * 32 + lane, end - 1);
+      const int slot =
+          static_cast<int>(__umulhi(static_cast<uint32_t>(e) * 2u, src.ps_magic) >> src.ps_shift);
+      off[k] = e - slot * src.ps;
+      page[k] = src.table[slot];
     }
   };
   if (count > 0) look_up(0);
@@ -193,17 +200,18 @@ __device__ __noinline__ int load_keys(const EvictParams &p, int b, int head, int
 #pragma unroll
     for (int k = 0; k < BATCH; ++k) {
       if (i + k >= count) break;
-      const int pg = static_cast<unsigned>(page[k]) < static_cast<unsigned>(c.num_pages) ? page[k] : 0;
-      const int64_t at = track_at(c, pg, head, off[k]);
-      order[k] = __ldcg(c.order + at);
-      w[k] = __ldcg(c.weight + at);
+      const int pg = static_cast<unsigned>(page[k]) < static_cast<unsigned>(src.num_pages) ? page[k] : 0;
+      const int64_t at = static_cast<int64_t>(pg) * src.page_stride + off[k];
+      order[k] = __ldcg(src.order + at);
+      w[k] = __ldcg(src.weight + at);
     }
     look_up(i + BATCH);          // the next pages, while the weights are on their way
 #pragma unroll
     for (int k = 0; k < BATCH; ++k) {
       if (i + k >= count) break;
-      const uint32_t key =
-          e0 + (i + k) * 32 + lane < end ? entry_key(p, order[k], w[k], recent_from) : 0u;
+      uint32_t key = w[k] > 0.f ? __float_as_uint(w[k]) : 0u;
+      if (order[k] < src.sinks || order[k] >= src.recent_from) key = kProtected;
+      if (e0 + (i + k) * 32 + lane >= end) key = 0u;
       keys[(i + k) * 32 + lane] = key;
       safe += __popc(__ballot_sync(0xffffffffu, key == kProtected));
     }
@@ -221,6 +229,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
   extern __shared__ uint32_t s_keys[];
   __shared__ __align__(16) uint32_t s_hist[kPasses][kBins], s_sum[2][kBins];
   __shared__ uint32_t s_safe;
+  __shared__ Found s_found;
   __shared__ int2 s_warp[2][WARPS];
   __shared__ int2 s_cta[3];
 
@@ -245,6 +254,11 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     const int take = room / THREADS;
     const int rounds = (per_warp / 32 + take - 1) / take;
     uint32_t *keys = s_keys + warp * take * 32;
+    const KeySource src = {c.table + b * c.table_stride,
+                           c.order + static_cast<int64_t>(head) * c.ps,
+                           c.weight + static_cast<int64_t>(head) * c.ps,
+                           c.hkv * c.ps, c.num_pages, c.ps, c.ps_magic, c.ps_shift,
+                           p.sinks, cut.recent_from};
     int safe = 0;
     // rows of a round, after reading its keys unless they are there
     auto rows_of = [&](int round, bool first) {
@@ -252,7 +266,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
       const int rows = (max(0, min(whi - e0, take * 32)) + 31) / 32;
       if (first || rounds > 1) {
         __syncwarp();
-        const int found = load_keys(p, b, head, cut.recent_from, e0, whi, rows, keys);
+        const int found = load_keys(src, e0, whi, rows, keys);
         if (first) safe += found;
       }
       return rows;
@@ -263,46 +277,61 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     __syncthreads();
     if (lane == 0) atomicAdd(&s_safe, static_cast<uint32_t>(safe));
 
-    Found f{0u, static_cast<uint32_t>(p.budget), 0u};
+    Found f{0u, static_cast<uint32_t>(p.budget), 0u, 1u};
     bool exact = false;        // the keys at or above the prefix are as many as wanted
 #pragma unroll 1
     for (int pass = 0; pass < kPasses && !exact; ++pass) {
-      const int shift = digit_shift(pass), bits = pass == kPasses - 1 ? 7 : 8;
+      // the keys that share the digits found so far, without the zeros and the protected ones: a range
+      const int shift = digit_shift(pass);
+      const uint32_t span = pass == 0 ? 0x7fffffffu : (1u << digit_shift(pass - 1)) - 1u;
+      const uint32_t low = max(f.prefix, 1u);
+      const uint32_t width = min(f.prefix + span, kProtected - 1u) - low;
       for (int round = 0; round < rounds; ++round) {
         const int rows = rows_of(round, false);
 #pragma unroll 4
         for (int i = 0; i < rows; ++i) {
           const uint32_t key = keys[i * 32 + lane];
-          if (key != 0 && key != kProtected && ((key ^ f.prefix) >> (shift + bits)) == 0)
-            atomicAdd(&s_hist[pass][(key >> shift) & ((1u << bits) - 1u)], 1u);
+          if (key - low <= width) atomicAdd(&s_hist[pass][(key - f.prefix) >> shift], 1u);
         }
       }
       const uint32_t *bins = s_hist[pass];
       if (CLUSTER) {
         cl.sync();
         if (tid < kBins) {
-          uint32_t sum = 0;
-          for (int k = 0; k < ranks; ++k) sum += *cl.map_shared_rank(&s_hist[pass][tid], k);
+          uint32_t sum = 0, part[kRanks];      // all of them asked for before the first is used
+#pragma unroll
+          for (int k = 0; k < kRanks; ++k)
+            part[k] = k < ranks ? *cl.map_shared_rank(&s_hist[pass][tid], k) : 0u;
+#pragma unroll
+          for (int k = 0; k < kRanks; ++k) sum += part[k];
           s_sum[pass & 1][tid] = sum;
         }
         bins = s_sum[pass & 1];
       }
-      uint32_t kept_safe = 0;
-      if (CLUSTER && pass == 0)
-        for (int k = 0; k < ranks; ++k) kept_safe += *cl.map_shared_rank(&s_safe, k);
       __syncthreads();
-      if (pass == 0) {
-        if (!CLUSTER) kept_safe = s_safe;
-        if (kept_safe >= f.want) {         // more protected entries than places: the first of them
-          f.prefix = kProtected;
-          f.ties = kept_safe;
-          exact = kept_safe == f.want;
-          break;
+      if (warp == 0) {
+        Found g = f;
+        g.more = 1;
+        uint32_t in_front = 0;
+        if (pass == 0)
+          in_front = CLUSTER ? __reduce_add_sync(
+                                   0xffffffffu, lane < ranks ? *cl.map_shared_rank(&s_safe, lane) : 0u)
+                             : s_safe;
+        if (in_front >= g.want) {          // more protected entries than places: the first of them
+          g.prefix = kProtected;
+          g.ties = in_front;
+          g.more = 0;
+        } else {
+          g.want -= in_front;
+          // every weight above 0 stays, and the first of the zeros
+          if (!descend(bins, pass, &g)) g.more = 0;
         }
-        f.want -= kept_safe;
+        if (lane == 0) s_found = g;
       }
-      if (!descend(bins, pass, &f)) break;   // every weight above 0 stays, and the first of the zeros
+      __syncthreads();
+      f = s_found;
       exact = f.want == f.ties;
+      if (!f.more) break;
     }
     if (exact && f.prefix == 0) f.prefix = 1;   // the zeros were not counted
     // kept: the keys at or above the prefix if exact, else those above it and the first f.want of those
@@ -357,29 +386,17 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     rank_now = tie_rank;
     for (int round = 0; round < rounds; ++round) {
       const int rows = rows_of(round, false), e0 = wlo + round * take * 32;
-      constexpr int BATCH = 4;
-      for (int i0 = 0; i0 < rows; i0 += BATCH) {
-        uint2 m[BATCH];
-        int row[BATCH];
-#pragma unroll
-        for (int k = 0; k < BATCH; ++k) {
-          const int i = i0 + k;
-          m[k] = make_uint2(0, 0);
-          if (i < rows) m[k] = rounds == 1 ? make_uint2(keys[i * 32], keys[i * 32 + 1]) : masks(e0, i);
-          row[k] = -1;
-          if (((m[k].x | m[k].y) >> lane) & 1u) {
-            // (page, place) as one number; a sequence with a bad page is left alone
-            int slot, off;
-            split_entry(c, e0 + i * 32 + lane, slot, off);
-            row[k] = c.table[b * c.table_stride + slot] * c.ps + off;
-          }
+#pragma unroll 4
+      for (int i = 0; i < rows; ++i) {
+        const uint2 m = rounds == 1 ? make_uint2(keys[i * 32], keys[i * 32 + 1]) : masks(e0, i);
+        const int e = e0 + i * 32 + lane;
+        if (m.x != 0) {
+          if ((m.x >> lane) & 1u) holes[to.x + __popc(m.x & below)] = e;
+          to.x += __popc(m.x);
         }
-#pragma unroll
-        for (int k = 0; k < BATCH; ++k) {
-          if ((m[k].x >> lane) & 1u) holes[to.x + __popc(m[k].x & below)] = row[k];
-          if ((m[k].y >> lane) & 1u) movers[to.y + __popc(m[k].y & below)] = row[k];
-          to.x += __popc(m[k].x);
-          to.y += __popc(m[k].y);
+        if (m.y != 0) {
+          if ((m.y >> lane) & 1u) movers[to.y + __popc(m.y & below)] = e;
+          to.y += __popc(m.y);
         }
       }
     }
@@ -391,7 +408,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
 
 // A warp takes kFlight moves (twice as many for head_dim 64, whose two rows fill half a warp) of a
 // (sequence, KV head) at a time: as many lanes move a weight and an ordinal each, then the warp copies the
-// rows, all loads before the first store; the next places are read while the rows are on their way.
+// rows, all loads before the first store.
 constexpr int kFlight = 8;
 
 template <int D>
@@ -421,22 +438,33 @@ __global__ void __launch_bounds__(kMoveWarps * 32, 3)
     const int32_t *movers = holes + p.moves_cap;
     uint8_t *base = (sub < VECS ? c.k : c.v) + head * c.head_bytes + (sub % VECS) * 16;
     int j0 = part * TAKE;
-    int dst = -1, src = 0;                     // rows (page * page size + place) of the lane's move
-    auto read_places = [&](int j) {
+    // The lane's move, -1: none. Its entries are read two batches ahead and its pages one. (The pages of a
+    // sequence that is not skipped were checked when they were claimed.)
+    int hole = -1, mover = -1, doff = -1, soff = 0, dpage = 0, spage = 0;
+    auto read_entries = [&](int j) {
       const bool in = lane < TAKE && j + lane < moves;
-      dst = in ? __ldcg(holes + j + lane) : -1;
-      src = in ? __ldcg(movers + j + lane) : 0;
+      hole = in ? __ldcg(holes + j + lane) : -1;
+      mover = in ? __ldcg(movers + j + lane) : -1;
     };
-    if (j0 < moves) read_places(j0);
+    auto read_pages = [&]() {
+      doff = -1;
+      if (hole >= 0) {
+        int slot;
+        split_entry(c, hole, slot, doff);
+        dpage = c.table[b * c.table_stride + slot];
+        split_entry(c, mover, slot, soff);
+        spage = c.table[b * c.table_stride + slot];
+      }
+    };
+    read_entries(j0);
+    read_pages();
+    read_entries(j0 + parts * TAKE);
     while (j0 < moves) {
       int64_t to = -1, from = 0, tw = 0;
       float weight = 0.f;
       int32_t order = 0;
-      const bool mine = dst >= 0;
+      const bool mine = doff >= 0;
       if (mine) {
-        int dpage, spage, doff, soff;
-        split_entry(c, dst, dpage, doff);
-        split_entry(c, src, spage, soff);
         to = dpage * c.page_bytes + doff * c.entry_bytes;
         from = spage * c.page_bytes + soff * c.entry_bytes;
         const int64_t fw = track_at(c, spage, head, soff);
@@ -452,7 +480,8 @@ __global__ void __launch_bounds__(kMoveWarps * 32, 3)
         if (i * PER + which < count) row[i] = ld_stream(base + s);
       }
       j0 += parts * TAKE;
-      if (j0 < moves) read_places(j0);
+      read_pages();
+      read_entries(j0 + parts * TAKE);
 #pragma unroll
       for (int i = 0; i < kFlight; ++i) {
         const int64_t d = __shfl_sync(0xffffffffu, to, i * PER + which);
@@ -475,7 +504,7 @@ cudaError_t launch_evict(const EvictParams &p, int num_sms, cudaStream_t stream)
   // as long as all of them find an SM and a share is more than 1024 entries. Long shares take the
   // largest blocks: two smaller ones would be put on one SM while others idle.
   int ranks = 1;
-  while (ranks < 8 &&
+  while (ranks < kRanks &&
          (c.cap > ranks * kKeyRoom || (c.cap > ranks * 1024 && items * ranks * 2 <= num_sms)))
     ranks *= 2;
   const int threads = c.cap > ranks * 4096 ? 1024 : 512;

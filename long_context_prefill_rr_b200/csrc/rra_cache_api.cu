@@ -90,8 +90,6 @@ rra_status resolve_sizes(const rra_cache *s, CacheView *c) {
   if (s->head_dim != 64 && s->head_dim != 128) return RRA_ERR_UNSUPPORTED;
   const int64_t cap = static_cast<int64_t>(s->max_pages) * s->page_size;
   if (cap > (1 << 30)) return RRA_ERR_UNSUPPORTED;
-  // rows of the cache (page * page_size + place) are counted in 31 bits
-  if (static_cast<int64_t>(s->num_pages) * s->page_size > INT_MAX) return RRA_ERR_UNSUPPORTED;
   const int g = s->heads_q / s->heads_kv;
   // units of work, table places and heads are counted in 32 bits
   const int64_t tiles = (g + rra::kDecodeHeads - 1) / rra::kDecodeHeads;
