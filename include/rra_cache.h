@@ -148,8 +148,9 @@ rra_status rra_cache_decode(const rra_cache *cache, const rra_view *q, const rra
  * entries at or behind `budget`, in ascending order, move into the places of the evicted ones
  * before it, in ascending order, with their weight and ordinal; nothing else moves, and entries at or
  * behind `budget` stay as they were. advance != 0 sets len[b] = budget; layers that share len
- * advance with the last one. Needs a tracked cache. Sequences with a page that the tables hold
- * more than once, or a bad one, are left as they are and flagged (their entries could not move apart). */
+ * advance with the last one. Needs a tracked cache. Sequences that share a page, with another or with
+ * themselves, or have a bad one are left as they are, since their entries could not move apart; this is
+ * flagged if one of the sharing sequences is over the budget. */
 rra_status rra_cache_evict(const rra_cache *cache, int budget, int sinks, int recent, int advance,
                            rra_stream_t stream);
 

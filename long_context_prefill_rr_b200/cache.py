@@ -8,7 +8,7 @@ before and behind the prefill of ``native``.
 
 Like ``native`` this is argument marshalling only, on torch CUDA tensors; every operator runs in the
 library's kernels. Calls run on the tensors' device, on its current stream unless ``stream`` is
-given, and do not synchronise.
+given, do not synchronise and are not recorded by autograd.
 """
 from __future__ import annotations
 
@@ -101,11 +101,6 @@ _NO_VIEW = (0, 0, 0, 0)
 _CODES = {torch.bfloat16: 0, torch.float16: 1}
 
 
-def _view4(t):
-    s = t.stride()
-    return t.data_ptr(), s[0], s[1], s[2]
-
-
 _here = contextlib.nullcontext()
 
 
@@ -128,6 +123,13 @@ def _raw_stream(stream, device):
     if stream.device != device:
         raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
     return stream.cuda_stream
+
+
+def _new(shape, dtype, device, stream):
+    x = torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None:
+        x.record_stream(stream)      # torch made it for the current stream
+    return x
 
 
 class RopeTable:
@@ -174,7 +176,19 @@ class RopeTable:
         self._ref = _c.byref(self.raw)
 
 
-def _fill_tokens(table, positions, q, k, v, q_out, k_out, v_out):
+def _rows_of(x, name, b, n, d, dtype, device):
+    """Address and strides of one tensor [b, heads, n, d], and its heads."""
+    shape, s = x.shape, x.stride()
+    if len(shape) != 4 or shape[0] != b or shape[2] != n or shape[3] != d or \
+            x.dtype is not dtype or x.device != device:
+        raise ValueError(f"{name} must be {dtype} [{b}, heads, {n}, {d}] on {device}, got "
+                         f"{x.dtype} {tuple(shape)} on {x.device}")
+    if s[3] != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return (x.data_ptr(), s[0], s[1], s[2]), shape[1]
+
+
+def _fill_tokens(table, positions, q, k, v, q_out, k_out, v_out, stream):
     """Checks the tensors of a call and packs them; returns (tokens, device, heads_q, outputs)."""
     first = k if k is not None else (q if q is not None else v)
     if first is None:
@@ -188,37 +202,35 @@ def _fill_tokens(table, positions, q, k, v, q_out, k_out, v_out):
     b, _, n, d = first.shape
     if d != table.head_dim:
         raise ValueError(f"head_dim is {d}, the table's is {table.head_dim}")
-    _need(positions, "positions", device, torch.int32, (table.axes, b, n))
-    heads = {"q": 0, "k": 0, "v": 0}
-    views, outs = [], []
-    for name, x, o in (("q", q, q_out), ("k", k, k_out), ("v", v, v_out)):
+    if positions.dtype is not torch.int32 or positions.device != device or \
+            positions.shape != (table.axes, b, n):
+        raise ValueError(f"positions must be torch.int32 {(table.axes, b, n)} on {device}, got "
+                         f"{positions.dtype} {tuple(positions.shape)} on {positions.device}")
+    heads, views, out_views, outs = [0, 0, 0], [], [], []
+    for i, (name, x, o) in enumerate((("q", q, q_out), ("k", k, k_out), ("v", v, v_out))):
         if x is None:
             if o is not None:
                 raise ValueError(f"{name}_out is given without {name}")
-            views.append(_NO_VIEW)
-            outs.append(None)
-            continue
-        shape = x.shape
-        if len(shape) != 4 or shape[0] != b or shape[2] != n or shape[3] != d or \
-                x.dtype is not dtype or x.device != device:
-            raise ValueError(f"{name} must be {dtype} [{b}, heads, {n}, {d}] on {device}, got "
-                             f"{x.dtype} {tuple(shape)} on {x.device}")
-        _rows(x, name)
-        heads[name] = shape[1]
-        views.append(_view4(x))
-        if o is True:
-            o = torch.empty(shape, dtype=dtype, device=device)
-        elif o is not None:
-            _need(o, name + "_out", device, dtype, shape)
-            _rows(o, name + "_out")
+            views += _NO_VIEW
+        else:
+            view, heads[i] = _rows_of(x, name, b, n, d, dtype, device)
+            views += view
+            if o is True:
+                o = _new(x.shape, dtype, device, stream)
         outs.append(o)
-    if k is not None and v is not None and heads["k"] != heads["v"]:
-        raise ValueError(f"k has {heads['k']} heads, v has {heads['v']}")
-    out_views = [_NO_VIEW if o is None else _view4(o) for o in outs]
-    t = _pack_tokens(b, heads["q"], heads["k"] or heads["v"], n, code, *_view4(positions),
-                     *views[0], *views[1], *views[2], *out_views[0], *out_views[1],
-                     *out_views[2])
-    return t, device, heads["q"], outs
+        if o is None:
+            out_views += _NO_VIEW
+            continue
+        view, h = _rows_of(o, name + "_out", b, n, d, dtype, device)
+        if h != heads[i]:
+            raise ValueError(f"{name}_out has {h} heads, {name} has {heads[i]}")
+        out_views += view
+    if k is not None and v is not None and heads[1] != heads[2]:
+        raise ValueError(f"k has {heads[1]} heads, v has {heads[2]}")
+    at = positions.stride()
+    t = _pack_tokens(b, heads[0], heads[1] or heads[2], n, code, positions.data_ptr(), *at,
+                     *views, *out_views)
+    return t, device, heads[0], outs
 
 
 def rope(table, positions, q=None, k=None, v=None, *, q_out=None, k_out=None, v_out=None,
@@ -231,7 +243,7 @@ def rope(table, positions, q=None, k=None, v=None, *, q_out=None, k_out=None, v_
     q_out = True if q is not None and q_out is None else q_out
     k_out = True if k is not None and k_out is None else k_out
     v_out = True if v is not None and v_out is None else v_out
-    t, device, _, outs = _fill_tokens(table, positions, q, k, v, q_out, k_out, v_out)
+    t, device, _, outs = _fill_tokens(table, positions, q, k, v, q_out, k_out, v_out, stream)
     raw = _raw_stream(stream, device)
     with _on(device):
         status = native.load().rra_rope_rotate(table._ref, t, 1 if inverse else 0, raw)
@@ -284,8 +296,8 @@ class PagedCache:
                         ("seen", seen)):
             if x is not None and not x.is_contiguous():
                 raise ValueError(f"{name} must be contiguous")
-        self.k, self.v, self.page_table, self.lengths = k, v, page_table, lengths
-        self.weight, self.order, self.seen = weight, order, seen
+        self._tensors = (k, v, page_table, lengths, weight, order, seen)
+        self.dtype = k.dtype
         self.device, self.batch, self.heads_q = device, b, heads_q
         s = k.stride()
         ptr = (lambda x: None if x is None else x.data_ptr())
@@ -302,6 +314,15 @@ class PagedCache:
             self.ws = torch.zeros(n, dtype=torch.uint8, device=device)
         self.raw.workspace, self.raw.workspace_bytes = self.ws.data_ptr(), n
         self._q_shape = (b, heads_q, d)
+
+    # the tensors that were given; read only, because the library holds their addresses
+    k = property(lambda self: self._tensors[0])
+    v = property(lambda self: self._tensors[1])
+    page_table = property(lambda self: self._tensors[2])
+    lengths = property(lambda self: self._tensors[3])
+    weight = property(lambda self: self._tensors[4])
+    order = property(lambda self: self._tensors[5])
+    seen = property(lambda self: self._tensors[6])
 
     @classmethod
     def allocate(cls, batch, max_len, heads_q, heads_kv, head_dim, *, page_size=64, dtype=None,
@@ -332,7 +353,7 @@ class PagedCache:
         q_out = True if q is not None and q_out is None else q_out
         if k is None or v is None:
             raise ValueError("k and v are required")
-        t, device, heads_q, outs = _fill_tokens(table, positions, q, k, v, q_out, k_out, v_out)
+        t, device, heads_q, outs = _fill_tokens(table, positions, q, k, v, q_out, k_out, v_out, stream)
         if device != self.device:
             raise ValueError(f"the cache is on {self.device}, the tokens are on {device}")
         if q is not None and heads_q != self.heads_q:
@@ -355,12 +376,12 @@ class PagedCache:
         fp32 [batch, heads_q], receives the logarithm of the softmax's denominator.
         ``add_weight=True`` adds the softmax weights to ``weight``."""
         shape = self._q_shape if q.dim() != 4 else self._q_shape[:2] + (1, self._q_shape[2])
-        _need(q, "q", self.device, self.k.dtype, shape)
+        _need(q, "q", self.device, self.dtype, shape)
         _rows(q, "q")
         if out is None:
-            out = torch.empty(shape, dtype=q.dtype, device=q.device)
+            out = _new(shape, q.dtype, q.device, stream)
         else:
-            _need(out, "out", self.device, self.k.dtype, shape)
+            _need(out, "out", self.device, self.dtype, shape)
             _rows(out, "out")
         if lse is not None:
             _need(lse, "lse", self.device, torch.float32, shape[:2])

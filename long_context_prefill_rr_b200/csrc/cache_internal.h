@@ -14,9 +14,10 @@ namespace rra {
 // Entries that one CTA step of the decode kernel covers (4 warps of 16), and the granule in which
 // its work is split over the grid.
 constexpr int kDecodeUnit = 64;
-// Query heads of a KV head that one warp of the decode kernel carries (the upper half of the 16
-// rows of its MMA tiles holds the low parts of the weights).
-constexpr int kDecodeHeads = 8;
+// Query heads of a KV head that one warp of the decode kernel carries: 8 fill half of its MMA tiles and leave
+// the other half to the low parts of their weights; more than 8 are cheaper 16 at a time than K and V
+// read once more.
+constexpr int decode_tile(int g) { return g > 8 ? 16 : 8; }
 
 // CTAs of the decode kernel that share an SM.
 constexpr int decode_ctas(int head_dim) { return head_dim == 128 ? 2 : 3; }
@@ -50,7 +51,7 @@ struct CacheLayout {
   size_t big;                      // logits [batch, hq, cap64], or the evict kernel's move lists
   size_t total;
   int grid;                        // CTAs of the decode kernel
-  int head_tiles;                  // ceil(g / kDecodeHeads)
+  int head_tiles;                  // ceil(g / decode_tile(g))
   int64_t cap64;                   // cap rounded up to kDecodeUnit
   int64_t moves;                   // places of one move list
 };
@@ -78,7 +79,7 @@ struct DecodeParams {
   int64_t q_batch, q_head, o_batch, o_head;   // bytes
   float *lse;
   float scale_log2;
-  int head_tiles, grid;
+  int tile, head_tiles, grid;
   float *part_o;
   float2 *part_ml;
   int32_t *counters;

@@ -19,7 +19,8 @@
 // k-steps; the columns of p.v may be permuted as well, so a thread takes 16 bytes of each of four
 // value rows and pairs up the rows' elements. The 8 query heads fill rows 0-7 of the 16-row MMA
 // tile. Rows 8-15 of the p.v product hold the low parts of the same weights (p = hi + lo, both 16-bit),
-// so the weights keep twice the bits of the element type at no cost.
+// so the weights keep twice the bits of the element type at no cost. With more than 8 heads to a KV head
+// rows 8-15 hold 8 more of them, and the low parts take a second product.
 //
 // Measured on the way (128K entries, 32 / 8 heads of 128, 537 MB; the copy rate gives 82 us): fragments
 // loaded straight into registers 107 us (64-byte requests, 56% of the load pipe's wavefronts); the
@@ -164,18 +165,20 @@ __device__ __forceinline__ void next_sequence(const CacheView &c, int items, Cur
   cur->units = units_of(cur->len);
 }
 
-template <class T, int D>
+// TILE: query heads of a KV head that a warp carries, 8 or 16.
+template <class T, int D, int TILE>
 __global__ void __launch_bounds__(kThreads, decode_ctas(D))
     paged_decode_kernel(const __grid_constant__ DecodeParams p) {
   constexpr int NJ = D / 32;        // 16-byte vectors of a key row per thread
   constexpr int NH = D / 64;        // 64-dimension halves of a value row
+  constexpr int HT = TILE / 8;      // heads of a thread: r and r + 8
   constexpr int S = kStages;
   constexpr uint32_t PITCH = kPitch<D>, STAGE = kStageBytes<D>;
   constexpr int ROW = D + 4;        // padded row of the merge buffer
-  static_assert(S <= 4 && S * STAGE >= kDecodeHeads * ROW * 4, "exist masks, merge buffer");
+  static_assert(S <= 4 && S * STAGE >= TILE * ROW * 4, "exist masks, merge buffer");
   extern __shared__ __align__(128) uint8_t s_ring[];
   __shared__ int s_scan[20];
-  __shared__ float s_m[kWarps][kDecodeHeads], s_l[kWarps][kDecodeHeads];
+  __shared__ float s_m[kWarps][TILE], s_l[kWarps][TILE];
 
   const CacheView &c = p.c;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -217,16 +220,19 @@ __global__ void __launch_bounds__(kThreads, decode_ctas(D))
     const int n = min(cur.units - unit0, end - pos);
     const int head = m / p.head_tiles;                   // KV head
     const int tile = m - head * p.head_tiles;
-    const int rows = min(kDecodeHeads, c.g - tile * kDecodeHeads);
-    const int h0 = head * c.g + tile * kDecodeHeads;     // first query head
+    const int rows = min(TILE, c.g - tile * TILE);
+    const int h0 = head * c.g + tile * TILE;     // first query head
     const int b = cur.b;
     const int key1 = min(cur.len, (unit0 + n) * kDecodeUnit);
 
-    uint4 qf[NJ];
+    uint4 qf[HT][NJ];
 #pragma unroll
-    for (int j = 0; j < NJ; ++j)
-      qf[j] = r < rows ? *reinterpret_cast<const uint4 *>(p.q + b * p.q_batch +
-                                                          (h0 + r) * p.q_head + (4 * j + t) * 16)
+    for (int h = 0; h < HT; ++h)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+        qf[h][j] = r + 8 * h < rows
+                       ? *reinterpret_cast<const uint4 *>(
+                             p.q + b * p.q_batch + (h0 + r + 8 * h) * p.q_head + (4 * j + t) * 16)
                        : make_uint4(0, 0, 0, 0);
 
     float acc[NH * 8][4];
@@ -234,7 +240,9 @@ __global__ void __launch_bounds__(kThreads, decode_ctas(D))
     for (int i = 0; i < NH * 8; ++i)
 #pragma unroll
       for (int q = 0; q < 4; ++q) acc[i][q] = 0.f;
-    float m_run = -INFINITY, l_run = 0.f;
+    float m_run[HT], l_run[HT];
+#pragma unroll
+    for (int h = 0; h < HT; ++h) m_run[h] = -INFINITY, l_run[h] = 0.f;
 
     // byte offset of entry kb + (lane & 15), or -1 if there is none
     auto place = [&](int kb) -> int64_t {
@@ -283,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, decode_ctas(D))
       __syncwarp();                    // the other lanes' copies of the stage have landed too
       const uint32_t kst = ring + now * STAGE + t * 16;
       const uint32_t vst = ring + now * STAGE + 16 * PITCH + r * 16;
-      // logits of head r for columns 2t, 2t + 1 of the first MMA tile and of the second
+      // logits of heads r and r + 8 for columns 2t, 2t + 1 of the first MMA tile and of the second
       float s[2][4];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -291,43 +299,55 @@ __global__ void __launch_bounds__(kThreads, decode_ctas(D))
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
           const uint4 kf = lds16(kst + (8 * i + entry_of(r >> 1, r & 1)) * PITCH + j * 64);
-          Elem<T>::mma(s[i], qf[j].x, 0u, qf[j].y, 0u, kf.x, kf.y);
-          Elem<T>::mma(s[i], qf[j].z, 0u, qf[j].w, 0u, kf.z, kf.w);
+          const uint4 q1 = HT == 2 ? qf[HT - 1][j] : make_uint4(0, 0, 0, 0);
+          Elem<T>::mma(s[i], qf[0][j].x, q1.x, qf[0][j].y, q1.y, kf.x, kf.y);
+          Elem<T>::mma(s[i], qf[0][j].z, q1.z, qf[0][j].w, q1.w, kf.z, kf.w);
         }
       }
-      float x[4];
+      float x[HT][4], mx[HT];
+      bool grows = false;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int e = entry_of(t, i & 1) + (i >> 1) * 8;
-        x[i] = (exist >> e) & 1u ? s[i >> 1][i & 1] * p.scale_log2 : -INFINITY;
-        if (p.logits && r < rows && kb + e < key1)
-          p.logits[(static_cast<int64_t>(b) * c.hq + h0 + r) * p.cap64 + kb + e] = x[i];
+      for (int h = 0; h < HT; ++h) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int e = entry_of(t, i & 1) + (i >> 1) * 8;
+          x[h][i] = (exist >> e) & 1u ? s[i >> 1][2 * h + (i & 1)] * p.scale_log2 : -INFINITY;
+          if (p.logits && r + 8 * h < rows && kb + e < key1)
+            p.logits[(static_cast<int64_t>(b) * c.hq + h0 + r + 8 * h) * p.cap64 + kb + e] = x[h][i];
+        }
+        mx[h] = fmaxf(fmaxf(x[h][0], x[h][1]), fmaxf(x[h][2], x[h][3]));
+        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
+        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
+        grows = grows || mx[h] > m_run[h];
       }
-      float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      if (__any_sync(0xffffffffu, mx > m_run)) {
-        const float m_new = fmaxf(m_run, mx);
-        // a row that has met no logit yet stays at -inf with sums of zero
-        const float alpha = m_new == -INFINITY ? 1.f : exp2f(m_run - m_new);
-        m_run = m_new;
-        l_run *= alpha;
+      if (__any_sync(0xffffffffu, grows)) {
+        float alpha[HT];
+#pragma unroll
+        for (int h = 0; h < HT; ++h) {
+          const float m_new = fmaxf(m_run[h], mx[h]);
+          // a row that has met no logit yet stays at -inf with sums of zero
+          alpha[h] = m_new == -INFINITY ? 1.f : exp2f(m_run[h] - m_new);
+          m_run[h] = m_new;
+          l_run[h] *= alpha[h];
+        }
 #pragma unroll
         for (int i = 0; i < NH * 8; ++i)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) acc[i][q] *= alpha;
+          for (int q = 0; q < 4; ++q) acc[i][q] *= alpha[q / 2 * (HT - 1)];
       }
-      const float base = m_run == -INFINITY ? 0.f : m_run;
-      float w[4];
+      uint32_t hi[HT][2], lo[HT][2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        w[i] = fast_exp2(x[i] - base);
-        l_run += w[i];
+      for (int h = 0; h < HT; ++h) {
+        const float base = m_run[h] == -INFINITY ? 0.f : m_run[h];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float w0 = fast_exp2(x[h][2 * i] - base), w1 = fast_exp2(x[h][2 * i + 1] - base);
+          l_run[h] += w0 + w1;
+          hi[h][i] = Elem<T>::pack(w0, w1);
+          const float2 f = Elem<T>::unpack(hi[h][i]);
+          lo[h][i] = Elem<T>::pack(w0 - f.x, w1 - f.y);
+        }
       }
-      const uint32_t hi0 = Elem<T>::pack(w[0], w[1]), hi1 = Elem<T>::pack(w[2], w[3]);
-      const float2 f0 = Elem<T>::unpack(hi0), f1 = Elem<T>::unpack(hi1);
-      const uint32_t lo0 = Elem<T>::pack(w[0] - f0.x, w[1] - f0.y);
-      const uint32_t lo1 = Elem<T>::pack(w[2] - f1.x, w[3] - f1.y);
 #pragma unroll
       for (int h = 0; h < NH; ++h) {
         uint4 vf[4];
@@ -341,9 +361,14 @@ __global__ void __launch_bounds__(kThreads, decode_ctas(D))
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const uint32_t pick = (e & 1) ? 0x7632u : 0x5410u;
-          Elem<T>::mma(acc[h * 8 + e], hi0, lo0, hi1, lo1,
-                       __byte_perm(v0[e >> 1], v1[e >> 1], pick),
-                       __byte_perm(v2[e >> 1], v3[e >> 1], pick));
+          const uint32_t b0 = __byte_perm(v0[e >> 1], v1[e >> 1], pick);
+          const uint32_t b1 = __byte_perm(v2[e >> 1], v3[e >> 1], pick);
+          if (HT == 1) {
+            Elem<T>::mma(acc[h * 8 + e], hi[0][0], lo[0][0], hi[0][1], lo[0][1], b0, b1);
+          } else {
+            Elem<T>::mma(acc[h * 8 + e], hi[0][0], hi[HT - 1][0], hi[0][1], hi[HT - 1][1], b0, b1);
+            Elem<T>::mma(acc[h * 8 + e], lo[0][0], lo[HT - 1][0], lo[0][1], lo[HT - 1][1], b0, b1);
+          }
         }
       }
       __syncwarp();                    // every lane's reads fed the MMAs above: the stage is free
@@ -352,25 +377,34 @@ __global__ void __launch_bounds__(kThreads, decode_ctas(D))
     __syncwarp();
 
     // ---- the warps' results meet in shared memory
-    l_run += __shfl_xor_sync(0xffffffffu, l_run, 1);
-    l_run += __shfl_xor_sync(0xffffffffu, l_run, 2);
-    if (t == 0) {
-      s_m[warp][r] = m_run;
-      s_l[warp][r] = l_run;
+#pragma unroll
+    for (int h = 0; h < HT; ++h) {
+      l_run[h] += __shfl_xor_sync(0xffffffffu, l_run[h], 1);
+      l_run[h] += __shfl_xor_sync(0xffffffffu, l_run[h], 2);
+      if (t == 0) {
+        s_m[warp][r + 8 * h] = m_run[h];
+        s_l[warp][r + 8 * h] = l_run[h];
+      }
     }
     // the thread's columns 2t and 2t + 1 of the permuted tiles are dimensions 16t .. 16t + 15 of
-    // each half; high and low parts of the weights are added here
+    // each half; with one head per thread the products of the low parts are added here
 #pragma unroll
-    for (int h = 0; h < NH; ++h)
+    for (int w = 0; w < HT; ++w)
 #pragma unroll
-      for (int q = 0; q < 2; ++q)
+      for (int h = 0; h < NH; ++h)
 #pragma unroll
-        for (int e = 0; e < 8; e += 4)
-          *reinterpret_cast<float4 *>(s_o(warp) + r * ROW + h * 64 + t * 16 + q * 8 + e) =
-              make_float4(acc[h * 8 + e][q] + acc[h * 8 + e][q + 2],
-                          acc[h * 8 + e + 1][q] + acc[h * 8 + e + 1][q + 2],
-                          acc[h * 8 + e + 2][q] + acc[h * 8 + e + 2][q + 2],
-                          acc[h * 8 + e + 3][q] + acc[h * 8 + e + 3][q + 2]);
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int e = 0; e < 8; e += 4) {
+            float y[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float *o = acc[h * 8 + e + k];
+              y[k] = HT == 1 ? o[q] + o[q + 2] : o[q + 2 * w];
+            }
+            *reinterpret_cast<float4 *>(s_o(warp) + (r + 8 * w) * ROW + h * 64 + t * 16 + q * 8 + e) =
+                make_float4(y[0], y[1], y[2], y[3]);
+          }
     __syncthreads();
 
     const int first_unit = cur.start + m * cur.units;
@@ -406,8 +440,8 @@ __global__ void __launch_bounds__(kThreads, decode_ctas(D))
           if (p.lse) p.lse[b * c.hq + h0 + row] = l2 * 0.6931471805599453f;
         }
       } else {
-        *reinterpret_cast<float4 *>(p.part_o + (slot * kDecodeHeads + row) * D + col) = o;
-        if (col == 0) p.part_ml[slot * kDecodeHeads + row] = make_float2(mt, l);
+        *reinterpret_cast<float4 *>(p.part_o + (slot * TILE + row) * D + col) = o;
+        if (col == 0) p.part_ml[slot * TILE + row] = make_float2(mt, l);
       }
     }
 
@@ -426,10 +460,10 @@ __global__ void __launch_bounds__(kThreads, decode_ctas(D))
           const int row = i / (D / 4), col = (i - row * (D / 4)) * 4;
           float mt = -INFINITY, l = 0.f;
           float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-          const float2 *ml = p.part_ml + (static_cast<int64_t>(item) + cta0) * kDecodeHeads + row;
+          const float2 *ml = p.part_ml + (static_cast<int64_t>(item) + cta0) * TILE + row;
           const float *po =
-              p.part_o + ((static_cast<int64_t>(item) + cta0) * kDecodeHeads + row) * D + col;
-          for (int k = cta0; k <= cta1; ++k, ml += kDecodeHeads, po += kDecodeHeads * D) {
+              p.part_o + ((static_cast<int64_t>(item) + cta0) * TILE + row) * D + col;
+          for (int k = cta0; k <= cta1; ++k, ml += TILE, po += TILE * D) {
             const float2 y = __ldcg(ml);
             const float4 x = __ldcg(reinterpret_cast<const float4 *>(po));
             const float mn = fmaxf(mt, y.x);
@@ -509,18 +543,20 @@ __global__ void __launch_bounds__(kWeightThreads)
   }
 }
 
-template <class T, int D>
+template <class T, int D, int TILE>
 cudaError_t launch_decode_t(const DecodeParams &p, cudaStream_t stream) {
   static std::atomic<uint64_t> allowed{0};
-  const cudaError_t e = allow_shared(paged_decode_kernel<T, D>, kRingBytes<D>, &allowed);
+  const auto kern = paged_decode_kernel<T, D, TILE>;
+  const cudaError_t e = allow_shared(kern, kRingBytes<D>, &allowed);
   if (e != cudaSuccess) return e;
-  return launch_dependent(paged_decode_kernel<T, D>, dim3(p.grid), kThreads, kRingBytes<D>, 1, stream,
-                          p);
+  return launch_dependent(kern, dim3(p.grid), kThreads, kRingBytes<D>, 1, stream, p);
 }
 
 template <class T>
 cudaError_t launch_decode_d(const DecodeParams &p, cudaStream_t stream) {
-  return p.c.d == 128 ? launch_decode_t<T, 128>(p, stream) : launch_decode_t<T, 64>(p, stream);
+  if (p.c.d == 128)
+    return p.tile == 8 ? launch_decode_t<T, 128, 8>(p, stream) : launch_decode_t<T, 128, 16>(p, stream);
+  return p.tile == 8 ? launch_decode_t<T, 64, 8>(p, stream) : launch_decode_t<T, 64, 16>(p, stream);
 }
 
 }  // namespace

@@ -14,7 +14,8 @@ static size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 CacheLayout cache_layout(const CacheView &c, bool tracked, int num_sms) {
   CacheLayout w{};
-  w.head_tiles = (c.g + kDecodeHeads - 1) / kDecodeHeads;
+  const int tile = decode_tile(c.g);
+  w.head_tiles = (c.g + tile - 1) / tile;
   const int64_t items = static_cast<int64_t>(c.batch) * c.hkv * w.head_tiles;
   w.cap64 = (static_cast<int64_t>(c.cap) + kDecodeUnit - 1) / kDecodeUnit * kDecodeUnit;
   // one CTA for every place on the SMs, but no more than there can be units of work
@@ -27,9 +28,9 @@ CacheLayout cache_layout(const CacheView &c, bool tracked, int num_sms) {
   w.counters = off;
   off = align_up(off + items * 4, 256);
   w.part_ml = off;
-  off = align_up(off + (items + w.grid) * kDecodeHeads * 8, 256);
+  off = align_up(off + (items + w.grid) * tile * 8, 256);
   w.part_o = off;
-  off = align_up(off + (items + w.grid) * kDecodeHeads * c.d * 4, 256);
+  off = align_up(off + (items + w.grid) * tile * c.d * 4, 256);
   w.lse2 = off;
   off = align_up(off + static_cast<size_t>(c.batch) * c.hq * 4, 256);
   if (tracked) {
@@ -91,10 +92,10 @@ rra_status resolve_sizes(const rra_cache *s, CacheView *c) {
   const int64_t cap = static_cast<int64_t>(s->max_pages) * s->page_size;
   if (cap > (1 << 30)) return RRA_ERR_UNSUPPORTED;
   const int g = s->heads_q / s->heads_kv;
-  // units of work, table places and heads are counted in 32 bits
-  const int64_t tiles = (g + rra::kDecodeHeads - 1) / rra::kDecodeHeads;
+  // units of work, table places and heads are counted in 32 bits, with room for one more round of CTAs
+  const int64_t tiles = (g + rra::decode_tile(g) - 1) / rra::decode_tile(g);
   const int64_t units = (cap + rra::kDecodeUnit - 1) / rra::kDecodeUnit;
-  if (s->batch > 0 && (static_cast<int64_t>(s->heads_kv) * tiles > INT_MAX / s->batch / units ||
+  if (s->batch > 0 && (static_cast<int64_t>(s->heads_kv) * tiles > (1 << 30) / s->batch / units ||
                        s->heads_q > INT_MAX / 1024 / s->batch ||
                        s->max_pages > INT_MAX / s->batch))
     return RRA_ERR_UNSUPPORTED;
@@ -360,6 +361,7 @@ rra_status rra_cache_decode(const rra_cache *cache, const rra_view *q, const rra
                           ? cache->softmax_scale
                           : 1.0f / sqrtf(static_cast<float>(cache->head_dim));
   p.scale_log2 = scale * 1.4426950408889634f;
+  p.tile = rra::decode_tile(p.c.g);
   p.head_tiles = w.head_tiles;
   p.grid = w.grid;
   p.part_o = at<float>(cache->workspace, w.part_o);

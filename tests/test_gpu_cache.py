@@ -587,6 +587,11 @@ def test_evict_leaves_shared_and_bad_pages_alone(cuda_device):
     order, seen = ordinals(p)
     p.table[0, 6], p.table[1, 1] = -1, p.table[1, 4].clone()   # a bad page; one page twice
     evicted(p, weights(p, "plain"), order, seen, 50, 2, 10, flagged=True)
+    # sequences within the budget may share, and are not the others' concern
+    p = Paged([100, 40, 40], 2, 2, 64, 16, seed=38, track=True)
+    order, seen = ordinals(p)
+    p.table[1, 0] = p.table[2, 0]
+    evicted(p, weights(p, "plain"), order, seen, 50, 2, 10)
     # a page behind a sequence's entries may be anybody's
     p = Paged([100, 100], 2, 2, 64, 16, seed=36, track=True, max_pages=9)
     order, seen = ordinals(p)
@@ -705,6 +710,28 @@ def test_captured_steps_follow_lengths(cuda_device):
         assert torch.equal(getattr(c, name), getattr(eager, name)), name
     c.check()
     eager.check()
+
+
+def test_allocate_and_what_it_holds(cuda_device):
+    c = cache.PagedCache.allocate(3, 100, 4, 2, 64, page_size=16, dtype=HF, track=True)
+    assert c.k.shape == (21, 2, 16, 64) and c.k.dtype == HF and c.page_table.shape == (3, 7)
+    assert not c.lengths.any() and c.weight.shape == c.order.shape == (21, 2, 16)
+    with pytest.raises(AttributeError):
+        c.lengths = torch.zeros(3, dtype=torch.int32, device="cuda")
+    out = c.decode(torch.ones(3, 4, 64, dtype=HF, device="cuda"))
+    assert not out.any()
+    none = cache.PagedCache.allocate(0, 100, 4, 2, 64)
+    assert none.decode(torch.ones(0, 4, 64, dtype=BF, device="cuda")).shape == (0, 4, 64)
+    for kw in (dict(weight=c.weight), dict(order=c.order, seen=c.seen)):
+        with pytest.raises(ValueError):
+            cache.PagedCache(c.k, c.v, c.page_table, c.lengths, heads_q=4, **kw)
+    with pytest.raises(ValueError):
+        cache.PagedCache(c.k, c.v.transpose(1, 2).contiguous().transpose(1, 2), c.page_table,
+                         c.lengths, heads_q=4)
+    with pytest.raises(ValueError):
+        cache.PagedCache(c.k, c.v, c.page_table.long(), c.lengths, heads_q=4)
+    with pytest.raises(native.RraError):
+        cache.PagedCache(c.k, c.v, c.page_table, c.lengths, heads_q=5)
 
 
 def test_other_streams(cuda_device):
