@@ -30,7 +30,8 @@
  *     length below 0 or beyond the page table counts as the nearest valid one, an entry on a page
  *     outside [0, num_pages) as absent.
  *   - The calls that share a workspace must not overlap on the GPU, nor must the calls that write a
- *     cache and any other call on that cache.
+ *     cache and any other call on that cache. A workspace may serve several caches of the same sizes (the
+ *     layers of a model); for other sizes it is laid out otherwise and has to be zero-filled again.
  */
 #ifndef RRA_CACHE_H_
 #define RRA_CACHE_H_

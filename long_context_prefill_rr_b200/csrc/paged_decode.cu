@@ -28,7 +28,9 @@
 // copy per row 106 (a warp issues its 32 copies one by one); this ring, whose copies cover whole rows,
 // 94. Two stages and two CTAs per SM (three for head_dim 64) keep 128 KB in flight; more bytes in flight
 // are slower (three stages 97, three CTAs 101; head_dim 64 with four stages and three CTAs 106
-// against 88).
+// against 88). 16 heads to a KV head take 70 us where two passes of 8 took 106 (4 x 40000 entries, 328 MB).
+// A call of 1000 entries takes 8 us, 2 of them the join of 16 pieces; reading eight pieces at a time
+// there made it slower (10: the longer code has to be fetched).
 #include <math.h>
 
 #include "cache_device.cuh"
@@ -495,10 +497,13 @@ __global__ void __launch_bounds__(kThreads, decode_ctas(D))
 }
 
 // weight[entry, KV head] += sum over the KV head's query heads of 2^(logit - lse2). A thread takes four
-// entries; the logits of the pass before are read once, most of them from L2.
+// entries; the logits of the pass before are read once, most of them from L2. Bound by its chain (length,
+// logits, page) in one round of blocks. 6 prompts, 223000 entries, 28 heads: 15 us behind cold caches, and 5
+// more for the logits' stores in a decode of 83; lanes on consecutive entries with single-word loads took
+// 6 us more.
 constexpr int kWeightThreads = 256;
 
-__global__ void __launch_bounds__(kWeightThreads)
+__global__ void __launch_bounds__(kWeightThreads, 6)
     add_weight_kernel(const __grid_constant__ DecodeParams p) {
   __shared__ int s_scan[20];
   const CacheView &c = p.c;

@@ -260,10 +260,12 @@ rra_status rra_rope_init(rra_rope *rope, int head_dim, int rotary_dim, int axes,
   r.axes = axes;
   r.pairing = pairing;
   if (!inv_freq && !(theta > 0.0 && isfinite(theta))) return RRA_ERR_INVALID_ARG;
-  for (int i = 0; i < pairs; ++i) {
-    const long double f =
-        inv_freq ? static_cast<long double>(inv_freq[i])
-                 : powl(static_cast<long double>(theta), -2.0L * i / rotary_dim);
+  // theta^(-2 i / rotary_dim) by multiplication: 64 bits of mantissa lose six of them at most
+  const long double step =
+      inv_freq ? 1.0L : powl(static_cast<long double>(theta), -2.0L / rotary_dim);
+  long double power = 1.0L;
+  for (int i = 0; i < pairs; ++i, power *= step) {
+    const long double f = inv_freq ? static_cast<long double>(inv_freq[i]) : power;
     if (!isfinite(f)) return RRA_ERR_INVALID_ARG;
     long double turns = f / (2.0L * 3.14159265358979323846264338327950288L);
     turns -= floorl(turns);                       // [0, 1)
