@@ -12,7 +12,6 @@ given, do not synchronise and are not recorded by autograd.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import struct
 
@@ -101,12 +100,12 @@ _NO_VIEW = (0, 0, 0, 0)
 _CODES = {torch.bfloat16: 0, torch.float16: 1}
 
 
-_here = contextlib.nullcontext()
-
-
-def _on(device):
-    """Makes the tensors' device current for a call (the library runs on the current one)."""
-    return _here if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+def _call(device, function, *args):
+    """Runs a library call with the tensors' device current (the library runs on the current one)."""
+    if torch.cuda.current_device() == device.index:
+        return function(*args)
+    with torch.cuda.device(device):
+        return function(*args)
 
 
 def _current_stream(device):
@@ -244,10 +243,8 @@ def rope(table, positions, q=None, k=None, v=None, *, q_out=None, k_out=None, v_
     k_out = True if k is not None and k_out is None else k_out
     v_out = True if v is not None and v_out is None else v_out
     t, device, _, outs = _fill_tokens(table, positions, q, k, v, q_out, k_out, v_out, stream)
-    raw = _raw_stream(stream, device)
-    with _on(device):
-        status = native.load().rra_rope_rotate(table._ref, t, 1 if inverse else 0, raw)
-    native._check(status, "rra_rope_rotate")
+    native._check(_call(device, native.load().rra_rope_rotate, table._ref, t, 1 if inverse else 0,
+                        _raw_stream(stream, device)), "rra_rope_rotate")
     outs = [o for o in outs if o is not None]
     return outs[0] if len(outs) == 1 else tuple(outs)
 
@@ -307,11 +304,10 @@ class PagedCache:
                           None, 0)
         self._ref = _c.byref(self.raw)
         self._lib = native.load()
-        with _on(device):
-            n = int(self._lib.rra_cache_workspace_bytes(self._ref))
-            if n == 0:
-                raise native.RraError(1, "rra_cache_workspace_bytes")
-            self.ws = torch.zeros(n, dtype=torch.uint8, device=device)
+        n = int(_call(device, self._lib.rra_cache_workspace_bytes, self._ref))
+        if n == 0:
+            raise native.RraError(1, "rra_cache_workspace_bytes")
+        self.ws = torch.zeros(n, dtype=torch.uint8, device=device)
         self.raw.workspace, self.raw.workspace_bytes = self.ws.data_ptr(), n
         self._q_shape = (b, heads_q, d)
 
@@ -362,12 +358,9 @@ class PagedCache:
             _need(new_len, "new_len", device, torch.int32, (self.batch,))
             if not new_len.is_contiguous():
                 raise ValueError("new_len must be contiguous")
-        raw = _raw_stream(stream, device)
-        with _on(device):
-            status = self._lib.rra_cache_append(
-                self._ref, table._ref, t, None if new_len is None else new_len.data_ptr(),
-                1 if advance else 0, raw)
-        native._check(status, "rra_cache_append")
+        native._check(_call(device, self._lib.rra_cache_append, self._ref, table._ref, t,
+                            None if new_len is None else new_len.data_ptr(), 1 if advance else 0,
+                            _raw_stream(stream, device)), "rra_cache_append")
         return outs[0] if k_out is None and v_out is None else tuple(outs)
 
     def decode(self, q, *, out=None, lse=None, add_weight=False, stream=None):
@@ -376,27 +369,30 @@ class PagedCache:
         fp32 [batch, heads_q], receives the logarithm of the softmax's denominator.
         ``add_weight=True`` adds the softmax weights to ``weight``."""
         shape = self._q_shape if q.dim() != 4 else self._q_shape[:2] + (1, self._q_shape[2])
-        _need(q, "q", self.device, self.dtype, shape)
-        _rows(q, "q")
+        device, dtype = self.device, self.dtype
+        sq = q.stride()
+        if q.shape != shape or q.dtype is not dtype or q.device != device or sq[-1] != 1:
+            _need(q, "q", device, dtype, shape)
+            _rows(q, "q")
         if out is None:
-            out = _new(shape, q.dtype, q.device, stream)
-        else:
-            _need(out, "out", self.device, self.dtype, shape)
+            out = _new(shape, dtype, device, stream)
+        so = out.stride()
+        if out.shape != shape or out.dtype is not dtype or out.device != device or so[-1] != 1:
+            _need(out, "out", device, dtype, shape)
             _rows(out, "out")
+        at = None
         if lse is not None:
-            _need(lse, "lse", self.device, torch.float32, shape[:2])
+            _need(lse, "lse", device, torch.float32, shape[:2])
             if not lse.is_contiguous():
                 raise ValueError("lse must be contiguous")
+            at = lse.data_ptr()
         if add_weight and not self.tracked:
             raise ValueError("add_weight needs a cache with weight, order and seen")
-        sq, so = q.stride(), out.stride()
-        raw = _raw_stream(stream, self.device)
-        with _on(self.device):
-            status = self._lib.rra_cache_decode(
-                self._ref, _pack_view(q.data_ptr(), sq[0], sq[1], 0),
-                _pack_view(out.data_ptr(), so[0], so[1], 0),
-                None if lse is None else lse.data_ptr(), 1 if add_weight else 0, raw)
-        native._check(status, "rra_cache_decode")
+        native._check(_call(device, self._lib.rra_cache_decode, self._ref,
+                            _pack_view(q.data_ptr(), sq[0], sq[1], 0),
+                            _pack_view(out.data_ptr(), so[0], so[1], 0), at,
+                            1 if add_weight else 0, _raw_stream(stream, device)),
+                      "rra_cache_decode")
         return out
 
     def evict(self, budget, *, sinks=0, recent=0, advance=True, stream=None):
@@ -406,16 +402,14 @@ class PagedCache:
             raise ValueError("evict needs a cache with weight, order and seen")
         if not all(0 <= x < 2 ** 31 for x in (budget, sinks, recent)):
             raise ValueError("budget, sinks and recent must fit 31 bits and not be negative")
-        raw = _raw_stream(stream, self.device)
-        with _on(self.device):
-            status = self._lib.rra_cache_evict(self._ref, budget, sinks, recent,
-                                               1 if advance else 0, raw)
-        native._check(status, "rra_cache_evict")
+        native._check(_call(self.device, self._lib.rra_cache_evict, self._ref, budget, sinks, recent,
+                            1 if advance else 0, _raw_stream(stream, self.device)),
+                      "rra_cache_evict")
 
     def check(self, stream=None):
         """Synchronises and raises if a call met a bad page, length or shared page since the last
         check (the error word is cleared)."""
-        raw, word = _raw_stream(stream, self.device), _c.c_uint32(0)
-        with _on(self.device):
-            st = self._lib.rra_check_device_status(self.ws.data_ptr(), raw, _c.byref(word))
+        word = _c.c_uint32(0)
+        st = _call(self.device, self._lib.rra_check_device_status, self.ws.data_ptr(),
+                   _raw_stream(stream, self.device), _c.byref(word))
         native._check(int(st), f"device status word {word.value:#x}")
