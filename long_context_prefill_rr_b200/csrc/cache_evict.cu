@@ -14,11 +14,12 @@
 //
 // Bound: 8 bytes (weight, ordinal) per entry and head read, and the moved rows read and written. Measured
 // (8 KV heads of 128, bf16): 32 sequences one entry over 2048, select 12 us and move 5; one of 128K cut to
-// 16K, 28 and 24 (the bytes take 17); eight of 32K cut to 8K, 38 and 75 (62). The move runs near the copy
-// rate; select is bound by its instructions, about 200 per 32 entries, and in short calls by the chain of
-// dependent steps (length, page, weight, four digits, ranks). A search bit by bit took 760 cycles a bit against
-// 1700 a digit; keys in registers, unrolled, were no faster than these rolled loops (each stretch of new
-// instructions has to be fetched first); a third launch that marked the pages beforehand cost 3 us.
+// 16K, 26 and 24 (the bytes take 17); eight of 32K cut to 8K, 36 and 75 (62). The move runs near the copy
+// rate; select is bound by its chain of dependent steps: length, page, weight, four digits and the ranks of
+// the lists, each with a barrier of the block or cluster. Taking the entries four at a time halved its
+// instructions and saved 2 us of 28; digits found bit by bit took 760 cycles a bit against 1700 a digit; keys
+// in registers, unrolled, were no faster than these rolled loops (each stretch of new instructions has to be
+// fetched first); a third launch that marked the pages beforehand cost 3 us.
 #include <cooperative_groups.h>
 
 #include <limits.h>
@@ -176,52 +177,59 @@ struct KeySource {
   int page_stride, num_pages, ps;
   uint32_t ps_magic, ps_shift;
   int sinks, recent_from;
+  bool four;                      // four consecutive entries from a multiple of four are one aligned vector
+
+  __device__ __forceinline__ int64_t at(int e) const {
+    const int slot = static_cast<int>(__umulhi(static_cast<uint32_t>(e) * 2u, ps_magic) >> ps_shift);
+    const int pg = table[slot];
+    // a page that is none (the sequence is left alone) reads as page 0
+    const int page = static_cast<unsigned>(pg) < static_cast<unsigned>(num_pages) ? pg : 0;
+    return static_cast<int64_t>(page) * page_stride + (e - slot * ps);
+  }
+  __device__ __forceinline__ uint32_t key(int32_t ordinal, float w) const {
+    if (ordinal < sinks || ordinal >= recent_from) return kProtected;
+    return w > 0.f ? __float_as_uint(w) : 0u;
+  }
 };
 
-// Keys of the entries e0 + 32 i + lane, i < count, to keys[32 i + lane]: what is kept first has the larger
-// key. Protected entries come first, then the weight: those not above zero are 0, positive floats order
-// like their bits and infinity is 0x7f800000, so 31 bits do. Entries at or past `end` get key 0. The
-// pages of a batch are looked up together, then its weights and ordinals; a page that is none (the
-// sequence is left alone) reads as page 0. Returns the protected entries of the warp.
-__device__ __noinline__ int load_keys(const KeySource src, int e0, int end, int count, uint32_t *keys) {
-  constexpr int BATCH = 4;
-  int safe = 0;
+// Keys of the entries e0 + 128 g + 4 lane + (0 .. 3), g < groups, to keys[128 g + 4 lane + ...]: what is kept
+// first has the larger key. Protected entries come first, then the weight: those not above zero are 0,
+// positive floats order like their bits and infinity is 0x7f800000, so 31 bits do. Entries at or past
+// `end` get key 0. Returns the protected entries of the lane.
+__device__ __noinline__ int load_keys(const KeySource src, int e0, int end, int groups, uint32_t *keys) {
   const int lane = threadIdx.x & 31;
-  int page[BATCH], off[BATCH];
-  auto look_up = [&](int i) {
-#pragma unroll
-    for (int k = 0; k < BATCH; ++k) {
-      if (i + k >= count) break;
-      const int e = min(e0 + (i + k) * 32 + lane, end - 1);
-      const int slot =
-          static_cast<int>(__umulhi(static_cast<uint32_t>(e) * 2u, src.ps_magic) >> src.ps_shift);
-      off[k] = e - slot * src.ps;
-      page[k] = src.table[slot];
-    }
-  };
-  if (count > 0) look_up(0);
+  int safe = 0;
+  int64_t next = 0;
+  if (groups > 0) next = src.at(min(e0 + lane * 4, end - 1));
 #pragma unroll 1
-  for (int i = 0; i < count; i += BATCH) {
-    int32_t order[BATCH];
-    float w[BATCH];
+  for (int g = 0; g < groups; ++g) {
+    const int e = e0 + g * 128 + lane * 4;
+    int32_t order[4];
+    float w[4];
+    if (src.four && e < end) {
+      // (the rest of a vector whose first entries exist lies in the same page)
+      const int4 o = __ldcg(reinterpret_cast<const int4 *>(src.order + next));
+      const float4 x = __ldcg(reinterpret_cast<const float4 *>(src.weight + next));
+      order[0] = o.x, order[1] = o.y, order[2] = o.z, order[3] = o.w;
+      w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+    } else {
+      int64_t at[4];
 #pragma unroll
-    for (int k = 0; k < BATCH; ++k) {
-      if (i + k >= count) break;
-      const int pg = static_cast<unsigned>(page[k]) < static_cast<unsigned>(src.num_pages) ? page[k] : 0;
-      const int64_t at = static_cast<int64_t>(pg) * src.page_stride + off[k];
-      order[k] = __ldcg(src.order + at);
-      w[k] = __ldcg(src.weight + at);
-    }
-    look_up(i + BATCH);          // the next pages, while the weights are on their way
+      for (int j = 0; j < 4; ++j) at[j] = src.at(min(e + j, end - 1));
 #pragma unroll
-    for (int k = 0; k < BATCH; ++k) {
-      if (i + k >= count) break;
-      uint32_t key = w[k] > 0.f ? __float_as_uint(w[k]) : 0u;
-      if (order[k] < src.sinks || order[k] >= src.recent_from) key = kProtected;
-      if (e0 + (i + k) * 32 + lane >= end) key = 0u;
-      keys[(i + k) * 32 + lane] = key;
-      safe += __popc(__ballot_sync(0xffffffffu, key == kProtected));
+      for (int j = 0; j < 4; ++j) {
+        order[j] = __ldcg(src.order + at[j]);
+        w[j] = __ldcg(src.weight + at[j]);
+      }
     }
+    next = src.at(min(e + 128, end - 1));   // the next page, while the weights are on their way
+    uint32_t key[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      key[j] = e + j < end ? src.key(order[j], w[j]) : 0u;
+      safe += key[j] == kProtected;
+    }
+    *reinterpret_cast<uint4 *>(keys + g * 128 + lane * 4) = make_uint4(key[0], key[1], key[2], key[3]);
   }
   return safe;
 }
@@ -233,7 +241,7 @@ template <int THREADS, bool CLUSTER>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     evict_select_kernel(const __grid_constant__ EvictParams p, int room) {
   constexpr int WARPS = THREADS / 32;
-  extern __shared__ uint32_t s_keys[];
+  extern __shared__ __align__(16) uint32_t s_keys[];
   __shared__ __align__(16) uint32_t s_hist[kPasses][kBins], s_sum[2][kBins];
   __shared__ uint32_t s_safe;
   __shared__ Found s_found;
@@ -255,32 +263,33 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
   const int n = cut.n;
   int moves = 0;
   if (n > p.budget) {   // the same for the whole cluster
-    // each CTA takes a run of entries, each of its warps a run of those, in rounds of `take` rows of 32
-    const int per_warp = (n + ranks * THREADS - 1) / (ranks * THREADS) * 32;
+    // each CTA takes a run of entries, each of its warps a run of those, in rounds of `take` groups of 128
+    const int per_warp = (n + ranks * THREADS * 4 - 1) / (ranks * THREADS * 4) * 128;
     const int wlo = min((rank * WARPS + warp) * per_warp, n), whi = min(wlo + per_warp, n);
-    const int take = room / THREADS;
-    const int rounds = (per_warp / 32 + take - 1) / take;
-    uint32_t *keys = s_keys + warp * take * 32;
+    const int take = room / (THREADS * 4);
+    const int rounds = (per_warp / 128 + take - 1) / take;
+    uint32_t *keys = s_keys + warp * take * 128;
     const KeySource src = {c.table + b * c.table_stride,
                            c.order + static_cast<int64_t>(head) * c.ps,
                            c.weight + static_cast<int64_t>(head) * c.ps,
                            c.hkv * c.ps, c.num_pages, c.ps, c.ps_magic, c.ps_shift,
-                           p.sinks, cut.recent_from};
+                           p.sinks, cut.recent_from, p.four != 0};
     int safe = 0;
-    // rows of a round, after reading its keys unless they are there
-    auto rows_of = [&](int round, bool first) {
-      const int e0 = wlo + round * take * 32;
-      const int rows = (max(0, min(whi - e0, take * 32)) + 31) / 32;
+    // groups of a round, after reading its keys unless they are there
+    auto groups_of = [&](int round, bool first) {
+      const int e0 = wlo + round * take * 128;
+      const int groups = (max(0, min(whi - e0, take * 128)) + 127) / 128;
       if (first || rounds > 1) {
-        __syncwarp();
-        const int found = load_keys(src, e0, whi, rows, keys);
+        const int found = load_keys(src, e0, whi, groups, keys);
         if (first) safe += found;
       }
-      return rows;
+      return groups;
     };
+    auto keys_of = [&](int g) { return *reinterpret_cast<const uint4 *>(keys + g * 128 + lane * 4); };
 
     // protected entries are counted apart, and entries of weight 0 not at all: both come in numbers
-    for (int round = 0; round < rounds; ++round) rows_of(round, true);
+    for (int round = 0; round < rounds; ++round) groups_of(round, true);
+    safe = __reduce_add_sync(0xffffffffu, safe);
     __syncthreads();
     if (lane == 0) atomicAdd(&s_safe, static_cast<uint32_t>(safe));
 
@@ -294,11 +303,14 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
       const uint32_t low = max(f.prefix, 1u);
       const uint32_t width = min(f.prefix + span, kProtected - 1u) - low;
       for (int round = 0; round < rounds; ++round) {
-        const int rows = rows_of(round, false);
-#pragma unroll 4
-        for (int i = 0; i < rows; ++i) {
-          const uint32_t key = keys[i * 32 + lane];
-          if (key - low <= width) atomicAdd(&s_hist[pass][(key - f.prefix) >> shift], 1u);
+        const int groups = groups_of(round, false);
+#pragma unroll 2
+        for (int g = 0; g < groups; ++g) {
+          const uint4 k = keys_of(g);
+          if (k.x - low <= width) atomicAdd(&s_hist[pass][(k.x - f.prefix) >> shift], 1u);
+          if (k.y - low <= width) atomicAdd(&s_hist[pass][(k.y - f.prefix) >> shift], 1u);
+          if (k.z - low <= width) atomicAdd(&s_hist[pass][(k.z - f.prefix) >> shift], 1u);
+          if (k.w - low <= width) atomicAdd(&s_hist[pass][(k.w - f.prefix) >> shift], 1u);
         }
       }
       const uint32_t *bins = s_hist[pass];
@@ -343,67 +355,84 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     if (exact && f.prefix == 0) f.prefix = 1;   // the zeros were not counted
     // kept: the keys at or above the prefix if exact, else those above it and the first f.want of those
     // equal to it
-    int tie_rank = 0;
+    const uint32_t least = exact ? f.prefix : f.prefix + 1u;
     int2 all;
+    auto ties_of = [&](int e, const uint4 &k) -> uint32_t {     // as a mask of the lane's four
+      const uint32_t m = (k.x == f.prefix ? 1u : 0u) | (k.y == f.prefix ? 2u : 0u) |
+                         (k.z == f.prefix ? 4u : 0u) | (k.w == f.prefix ? 8u : 0u);
+      return m & ((1u << max(0, min(whi - e, 4))) - 1u);
+    };
+    int tie_rank = 0;
     if (!exact) {
       int ties = 0;
       for (int round = 0; round < rounds; ++round) {
-        const int rows = rows_of(round, false), e0 = wlo + round * take * 32 + lane;
-        for (int i = 0; i < rows; ++i)
-          ties += __popc(__ballot_sync(0xffffffffu, e0 + i * 32 < whi && keys[i * 32 + lane] == f.prefix));
+        const int groups = groups_of(round, false), e0 = wlo + round * take * 128 + lane * 4;
+        for (int g = 0; g < groups; ++g) ties += __popc(ties_of(e0 + g * 128, keys_of(g)));
       }
+      ties = __reduce_add_sync(0xffffffffu, ties);
       tie_rank = prefix_of_warps<WARPS, CLUSTER>(make_int2(ties, 0), s_warp[0], &s_cta[0], &all).x;
     }
-    // Rows of 32: `kept` as a mask, which against the budget gives the places to fill and the entries to
-    // move. The masks are kept in the place of the row's first keys for the second pass, when the ranks of
-    // the first are known.
-    const uint32_t below = (1u << lane) - 1u;
     int32_t *holes = p.moves + static_cast<int64_t>(item) * 2 * p.moves_cap;
     int32_t *movers = holes + p.moves_cap;
     int rank_now = tie_rank;
-    auto masks = [&](int e0, int i) {
-      const int first = e0 + i * 32;
-      const uint32_t key = keys[i * 32 + lane];
-      const uint32_t in = whi - first >= 32 ? 0xffffffffu : (1u << (whi - first)) - 1u;
-      const uint32_t front =
-          p.budget >= first + 32 ? 0xffffffffu : (p.budget > first ? (1u << (p.budget - first)) - 1u : 0u);
-      uint32_t kept = __ballot_sync(0xffffffffu, exact ? key >= f.prefix : key > f.prefix) & in;
+    // Masks of the lane's four entries from e: the places to fill (x) and the entries to move (y).
+    auto masks = [&](int e, const uint4 &k) {
+      uint32_t kept = (k.x >= least ? 1u : 0u) | (k.y >= least ? 2u : 0u) | (k.z >= least ? 4u : 0u) |
+                      (k.w >= least ? 8u : 0u);
+      const uint32_t in = (1u << max(0, min(whi - e, 4))) - 1u;
+      const uint32_t front = (1u << max(0, min(p.budget - e, 4))) - 1u;
       if (!exact) {
-        const uint32_t tied = __ballot_sync(0xffffffffu, key == f.prefix) & in;
-        kept |= __ballot_sync(0xffffffffu, ((tied >> lane) & 1u) != 0 &&
-                                               rank_now + __popc(tied & below) <
-                                                   static_cast<int>(f.want));
-        rank_now += __popc(tied);
+        const uint32_t tied = ties_of(e, k);
+        const int before = static_cast<int>(lane_prefix(__popc(tied), lane));
+        int left = static_cast<int>(f.want) - rank_now - before;   // ties of this lane that stay
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if ((tied >> j) & 1u) {
+            if (left > 0) kept |= 1u << j;
+            --left;
+          }
+        rank_now += __shfl_sync(0xffffffffu, before + __popc(tied), 31);
       }
+      kept &= in;
       return make_uint2(in & front & ~kept, kept & ~front);
     };
     int2 seen = make_int2(0, 0);
     for (int round = 0; round < rounds; ++round) {
-      const int rows = rows_of(round, false), e0 = wlo + round * take * 32;
-#pragma unroll 4
-      for (int i = 0; i < rows; ++i) {
-        const uint2 m = masks(e0, i);
+      const int groups = groups_of(round, false), e0 = wlo + round * take * 128 + lane * 4;
+      for (int g = 0; g < groups; ++g) {
+        const uint2 m = masks(e0 + g * 128, keys_of(g));
         seen.x += __popc(m.x);
         seen.y += __popc(m.y);
-        if (rounds == 1 && lane < 2) keys[i * 32 + lane] = lane == 0 ? m.x : m.y;
       }
     }
+    seen.x = __reduce_add_sync(0xffffffffu, seen.x);
+    seen.y = __reduce_add_sync(0xffffffffu, seen.y);
     int2 to = prefix_of_warps<WARPS, CLUSTER>(seen, s_warp[1], &s_cta[1], &all);
     moves = all.x;
     rank_now = tie_rank;
     for (int round = 0; round < rounds; ++round) {
-      const int rows = rows_of(round, false), e0 = wlo + round * take * 32;
-#pragma unroll 4
-      for (int i = 0; i < rows; ++i) {
-        const uint2 m = rounds == 1 ? make_uint2(keys[i * 32], keys[i * 32 + 1]) : masks(e0, i);
-        const int e = e0 + i * 32 + lane;
-        if (m.x != 0) {
-          if ((m.x >> lane) & 1u) holes[to.x + __popc(m.x & below)] = e;
-          to.x += __popc(m.x);
+      const int groups = groups_of(round, false), e0 = wlo + round * take * 128 + lane * 4;
+      for (int g = 0; g < groups; ++g) {
+        const int e = e0 + g * 128;
+        const uint2 m = masks(e, keys_of(g));
+        // both ranks in one prefix: a group has 128 entries
+        const uint32_t mine = __popc(m.x) | (__popc(m.y) << 16);
+        const uint32_t before = lane_prefix(mine, lane);
+        const uint32_t total = __shfl_sync(0xffffffffu, before + mine, 31);
+        // a group lies before the budget or behind it, but for one
+        if (total & 0xffffu) {
+          int32_t *h = holes + to.x + static_cast<int>(before & 0xffffu);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if ((m.x >> j) & 1u) *h++ = e + j;
+          to.x += static_cast<int>(total & 0xffffu);
         }
-        if (m.y != 0) {
-          if ((m.y >> lane) & 1u) movers[to.y + __popc(m.y & below)] = e;
-          to.y += __popc(m.y);
+        if (total >> 16) {
+          int32_t *v = movers + to.y + static_cast<int>(before >> 16);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if ((m.y >> j) & 1u) *v++ = e + j;
+          to.y += static_cast<int>(total >> 16);
         }
       }
     }
@@ -515,10 +544,10 @@ cudaError_t launch_evict(const EvictParams &p, int num_sms, cudaStream_t stream)
          (c.cap > ranks * kKeyRoom || (c.cap > ranks * 1024 && items * ranks * 2 <= num_sms)))
     ranks *= 2;
   const int threads = c.cap > ranks * 4096 ? 1024 : 512;
-  // keys per CTA, in whole rows of 32 for each warp
+  // keys per CTA, in whole groups of 128 for each warp
   const int64_t share = (static_cast<int64_t>(c.cap) + ranks - 1) / ranks;
-  const int room =
-      static_cast<int>(std::min<int64_t>(kKeyRoom, (share + threads - 1) / threads * threads));
+  const int room = static_cast<int>(
+      std::min<int64_t>(kKeyRoom, (share + threads * 4 - 1) / (threads * 4) * (threads * 4)));
   static std::atomic<uint64_t> allowed[4];
   const auto kern =
       ranks > 1 ? (threads == 1024 ? evict_select_kernel<1024, true> : evict_select_kernel<512, true>)

@@ -91,6 +91,7 @@ struct DecodeParams {
 struct EvictParams {
   CacheView c;
   int budget, sinks, recent, advance;
+  int four;                    // weights and ordinals may be read four at a time
   uint32_t *epoch;             // calls so far; a call marks what it finds with epoch + 1
   uint32_t *skip, *tags;       // [batch]: the call that left the sequence alone; the current one
   int32_t *lens, *plan;        // [batch] lengths; [batch * hkv] moves

@@ -393,6 +393,8 @@ rra_status rra_cache_evict(const rra_cache *cache, int budget, int sinks, int re
   p.sinks = sinks;
   p.recent = recent;
   p.advance = advance != 0;
+  // a page's rows of weights then start at multiples of 16 bytes
+  p.four = cache->page_size % 4 == 0 && aligned16(cache->weight) && aligned16(cache->order);
   p.epoch = at<uint32_t>(cache->workspace, w.epoch);
   p.skip = at<uint32_t>(cache->workspace, w.skip);
   p.tags = at<uint32_t>(cache->workspace, w.tags);

@@ -558,6 +558,19 @@ def test_evict_long(cuda_device, layout, dtype, lens, budget, kind):
     evicted(p, weights(p, kind), order, seen, budget, 4, 700)
 
 
+def test_evict_weights_off_a_vector(cuda_device):
+    """Weights and ordinals that start 4 and 8 bytes past a multiple of 16 are read one by one."""
+    p = Paged([700, 333], 2, 2, 64, 16, seed=39, track=True)
+    order, seen = ordinals(p)
+    n = p.cache.weight.numel()
+    w = torch.zeros(n + 4, device="cuda")[1:n + 1].view(p.cache.weight.shape)
+    o = torch.zeros(n + 4, dtype=torch.int32, device="cuda")[2:n + 2].view(p.cache.weight.shape)
+    p.cache = cache.PagedCache(p.k, p.v, p.table, p.lens, heads_q=2, weight=w, order=o, seen=seen)
+    evicted(p, weights(p, "ties"), order, seen, 300, 5, 50)
+    p.lens.fill_(300)
+    run_decode(p, add_weight=True)
+
+
 def test_evict_shares_longer_than_shared_memory(cuda_device):
     """Keys that do not fit the cluster's shared memory are read again for every digit."""
     n = 8 * 32768 + 12345
