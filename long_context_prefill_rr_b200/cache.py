@@ -177,14 +177,27 @@ class RopeTable:
 
 def _rows_of(x, name, b, n, d, dtype, device):
     """Address and strides of one tensor [b, heads, n, d], and its heads."""
-    shape, s = x.shape, x.stride()
-    if len(shape) != 4 or shape[0] != b or shape[2] != n or shape[3] != d or \
-            x.dtype is not dtype or x.device != device:
-        raise ValueError(f"{name} must be {dtype} [{b}, heads, {n}, {d}] on {device}, got "
-                         f"{x.dtype} {tuple(shape)} on {x.device}")
-    if s[3] != 1:
-        raise ValueError(f"{name}: the last dimension must be contiguous")
-    return (x.data_ptr(), s[0], s[1], s[2]), shape[1]
+    if x.dim() == 4:
+        xb, heads, xn, xd = x.shape
+        s0, s1, s2, s3 = x.stride()
+        if xb == b and xn == n and xd == d and s3 == 1 and x.dtype is dtype and x.device == device:
+            return (x.data_ptr(), s0, s1, s2), heads
+        if xb == b and xn == n and xd == d and x.dtype is dtype and x.device == device:
+            raise ValueError(f"{name}: the last dimension must be contiguous")
+    raise ValueError(f"{name} must be {dtype} [{b}, heads, {n}, {d}] on {device}, got {x.dtype} "
+                     f"{tuple(x.shape)} on {x.device}")
+
+
+def _out_of(o, x, name, b, heads, n, d, dtype, device, stream):
+    """An output and its view: none (None), the caller's, or a new one (True)."""
+    if o is None:
+        return None, _NO_VIEW
+    if o is True:
+        o = _new(x.shape, dtype, device, stream)
+    view, h = _rows_of(o, name, b, n, d, dtype, device)
+    if h != heads:
+        raise ValueError(f"{name} has {h} heads, its input has {heads}")
+    return o, view
 
 
 def _fill_tokens(table, positions, q, k, v, q_out, k_out, v_out, stream):
@@ -205,31 +218,30 @@ def _fill_tokens(table, positions, q, k, v, q_out, k_out, v_out, stream):
             positions.shape != (table.axes, b, n):
         raise ValueError(f"positions must be torch.int32 {(table.axes, b, n)} on {device}, got "
                          f"{positions.dtype} {tuple(positions.shape)} on {positions.device}")
-    heads, views, out_views, outs = [0, 0, 0], [], [], []
-    for i, (name, x, o) in enumerate((("q", q, q_out), ("k", k, k_out), ("v", v, v_out))):
-        if x is None:
-            if o is not None:
-                raise ValueError(f"{name}_out is given without {name}")
-            views += _NO_VIEW
-        else:
-            view, heads[i] = _rows_of(x, name, b, n, d, dtype, device)
-            views += view
-            if o is True:
-                o = _new(x.shape, dtype, device, stream)
-        outs.append(o)
-        if o is None:
-            out_views += _NO_VIEW
-            continue
-        view, h = _rows_of(o, name + "_out", b, n, d, dtype, device)
-        if h != heads[i]:
-            raise ValueError(f"{name}_out has {h} heads, {name} has {heads[i]}")
-        out_views += view
-    if k is not None and v is not None and heads[1] != heads[2]:
-        raise ValueError(f"k has {heads[1]} heads, v has {heads[2]}")
-    at = positions.stride()
-    t = _pack_tokens(b, heads[0], heads[1] or heads[2], n, code, positions.data_ptr(), *at,
-                     *views, *out_views)
-    return t, device, heads[0], outs
+    p0, p1, p2 = positions.stride()
+    heads_q = heads_kv = 0
+    q_view = k_view = v_view = q_to = k_to = v_to = _NO_VIEW
+    if q is not None:
+        q_view, heads_q = _rows_of(q, "q", b, n, d, dtype, device)
+        q_out, q_to = _out_of(q_out, q, "q_out", b, heads_q, n, d, dtype, device, stream)
+    elif q_out is not None:
+        raise ValueError("q_out is given without q")
+    if k is not None:
+        k_view, heads_kv = _rows_of(k, "k", b, n, d, dtype, device)
+        k_out, k_to = _out_of(k_out, k, "k_out", b, heads_kv, n, d, dtype, device, stream)
+    elif k_out is not None:
+        raise ValueError("k_out is given without k")
+    if v is not None:
+        v_view, heads_v = _rows_of(v, "v", b, n, d, dtype, device)
+        if k is not None and heads_v != heads_kv:
+            raise ValueError(f"k has {heads_kv} heads, v has {heads_v}")
+        heads_kv = heads_v
+        v_out, v_to = _out_of(v_out, v, "v_out", b, heads_v, n, d, dtype, device, stream)
+    elif v_out is not None:
+        raise ValueError("v_out is given without v")
+    t = _pack_tokens(b, heads_q, heads_kv, n, code, positions.data_ptr(), p0, p1, p2, *q_view,
+                     *k_view, *v_view, *q_to, *k_to, *v_to)
+    return t, device, heads_q, (q_out, k_out, v_out)
 
 
 def rope(table, positions, q=None, k=None, v=None, *, q_out=None, k_out=None, v_out=None,
@@ -308,6 +320,8 @@ class PagedCache:
         if n == 0:
             raise native.RraError(1, "rra_cache_workspace_bytes")
         self.ws = torch.zeros(n, dtype=torch.uint8, device=device)
+        if not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream(device).synchronize()   # ready for calls on any stream
         self.raw.workspace, self.raw.workspace_bytes = self.ws.data_ptr(), n
         self._q_shape = (b, heads_q, d)
 
@@ -361,7 +375,7 @@ class PagedCache:
         native._check(_call(device, self._lib.rra_cache_append, self._ref, table._ref, t,
                             None if new_len is None else new_len.data_ptr(), 1 if advance else 0,
                             _raw_stream(stream, device)), "rra_cache_append")
-        return outs[0] if k_out is None and v_out is None else tuple(outs)
+        return outs[0] if k_out is None and v_out is None else outs
 
     def decode(self, q, *, out=None, lse=None, add_weight=False, stream=None):
         """Attention of one new token per sequence, q [batch, heads_q, head_dim] or
