@@ -538,12 +538,15 @@ cudaError_t launch_evict(const EvictParams &p, int num_sms, cudaStream_t stream)
   const int items = c.batch * c.hkv;
   // One block where there are blocks enough or little to share, else up to eight that share the work of one,
   // as long as all of them find an SM and a share is more than 1024 entries. Long shares take the
-  // largest blocks: two smaller ones would be put on one SM while others idle.
+  // largest blocks: two smaller ones would be put on one SM while others idle. But clusters of eight of them find
+  // places on only four fifths of the SMs (a cluster stays within a group of SMs); more than those would
+  // wait for a second round, 90 us against 86 for the smaller blocks (five sequences of up to 128K, 4 heads).
   int ranks = 1;
   while (ranks < kRanks &&
          (c.cap > ranks * kKeyRoom || (c.cap > ranks * 1024 && items * ranks * 2 <= num_sms)))
     ranks *= 2;
-  const int threads = c.cap > ranks * 4096 ? 1024 : 512;
+  const bool crowded = ranks == kRanks && items * ranks > num_sms * 4 / 5;
+  const int threads = c.cap > ranks * 4096 && !crowded ? 1024 : 512;
   // keys per CTA, in whole groups of 128 for each warp
   const int64_t share = (static_cast<int64_t>(c.cap) + ranks - 1) / ranks;
   const int room = static_cast<int>(

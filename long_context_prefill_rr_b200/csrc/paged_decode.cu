@@ -26,9 +26,10 @@
 // loaded straight into registers 107 us (64-byte requests, 56% of the load pipe's wavefronts); the
 // same loads through cp.async into places private to each thread 136; a ring of rows filled by one bulk
 // copy per row 106 (a warp issues its 32 copies one by one); this ring, whose copies cover whole rows,
-// 94. Two stages and two CTAs per SM (three for head_dim 64) keep 128 KB in flight; more bytes in flight
-// are slower (three stages 97, three CTAs 101; head_dim 64 with four stages and three CTAs 106
-// against 88). 16 heads to a KV head take 70 us where two passes of 8 took 106 (4 x 40000 entries, 328 MB).
+// 92, and 90 with the rows marked to leave L2 first. Two stages and two CTAs per SM (three for head_dim
+// 64) keep 128 KB in flight; more bytes in flight are slower (three stages 97, three CTAs 101;
+// head_dim 64 with four stages and three CTAs 106 against 88). 16 heads to a KV head take 66 us where
+// two passes of 8 took 106 (4 x 40000 entries, 328 MB).
 // A call of 1000 entries takes 8 us, 2 of them the join of 16 pieces; reading eight pieces at a time
 // there made it slower (10: the longer code has to be fetched).
 #include <math.h>
@@ -53,9 +54,16 @@ constexpr uint32_t kStageBytes = 32 * kPitch<D>;
 template <int D>
 constexpr size_t kRingBytes = static_cast<size_t>(kWarps) * kStages * kStageBytes<D>;
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool valid) {
+// Keys and values are read once: they leave L2 first, before the logits and pieces that are read again.
+__device__ __forceinline__ uint64_t once_policy() {
+  uint64_t policy;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+  return policy;
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool valid, uint64_t policy) {
   const int n = valid ? 16 : 0;   // 0: nothing is read, the place is filled with zeros
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst),
+               "l"(src), "r"(n), "l"(policy)
                : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -191,6 +199,7 @@ __global__ void __launch_bounds__(kThreads, decode_ctas(D))
   // the merge buffer of a warp lies over its ring, which is idle then
   auto s_o = [&](int w) { return reinterpret_cast<float *>(s_ring + w * S * STAGE); };
 
+  const uint64_t policy = once_policy();
   grid_dependency_wait();
   grid_dependents_go();
   // sequences without entries, and lengths outside the table
@@ -266,8 +275,8 @@ __global__ void __launch_bounds__(kThreads, decode_ctas(D))
       for (int i = 0; i < 16 / ROWS; ++i) {
         const int64_t o = __shfl_sync(0xffffffffu, at, i * ROWS + lane / LANES);
         const int64_t from = o >= 0 ? o : 0;
-        copy16(dst + i * ROWS * PITCH, kh + from, o >= 0);
-        copy16(dst + (16 + i * ROWS) * PITCH, vh + from, o >= 0);
+        copy16(dst + i * ROWS * PITCH, kh + from, o >= 0, policy);
+        copy16(dst + (16 + i * ROWS) * PITCH, vh + from, o >= 0, policy);
       }
       return __ballot_sync(0xffffffffu, at >= 0) & 0xffffu;
     };
