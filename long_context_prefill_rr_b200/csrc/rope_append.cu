@@ -10,10 +10,10 @@
 // Memory bound: every row is read once and written once (twice where the prefill's copy and the
 // cache both want it). A thread owns one unit of 16 dimensions (two 16-byte vectors: for halves one
 // from each half, 8 pairs) of one token and walks over heads, so the eight sines and cosines are
-// taken once for all of them. Measured (65536 tokens, 28 + 4 heads of 128, bf16, 1.07 GB): 177 us, 93% of
+// taken once for all of them. Measured (65536 tokens, 28 + 4 heads of 128, bf16, 1.07 GB): 175 us, 94% of
 // the copy rate; with four blocks per SM 187, with two heads in flight per thread and spills 181, with
 // sincospif in place of the series and four heads in flight 195. 7500 tokens, a quarter of them padding,
-// into pages (104 MB): 28 us against 16 for the bytes; it is the reads of lengths, pages and positions in
+// into pages (104 MB): 25 us against 16 for the bytes; it is the reads of lengths, pages and positions in
 // front of the first row, and blocks of padding that leave their place idle, that cost there.
 #include "cache_device.cuh"
 

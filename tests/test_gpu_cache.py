@@ -215,7 +215,8 @@ class Paged:
         empty = np.isinf(rlse)
         assert np.array_equal(f64(lse)[empty], rlse[empty])
         assert not f64(out)[empty].any()
-        err, ok = np.abs(f64(lse) - rlse)[~empty], ~empty
+        ok = ~empty
+        err = np.abs(f64(lse)[ok] - rlse[ok])
         assert (err <= delta[ok] + 2.0 ** -21 * (1 + np.abs(rlse[ok]))).all(), float(err.max())
         if weight is not None:
             g = self.hq // self.k.shape[1]
@@ -542,6 +543,7 @@ def weights(p, kind, seed=0):
 @pytest.mark.parametrize("lens,budget,sinks,recent,ps,hkv,d", [
     ([1, 0, 2, 3], 1, 0, 1, 1, 2, 64), ([64, 65, 66, 200], 64, 4, 20, 16, 3, 128),
     ([500, 31, 32, 33], 32, 0, 0, 7, 2, 64), ([1500, 1499], 1499, 100, 1399, 20, 1, 128),
+    (list(range(300)), 40, 3, 9, 8, 3, 64),
     ([900], 450, 450, 0, 64, 2, 64), ([9000, 100, 4500], 2000, 16, 500, 64, 2, 64)])
 def test_evict(cuda_device, kind, lens, budget, sinks, recent, ps, hkv, d):
     p = Paged(lens, hkv, hkv, d, ps, seed=30, track=True)
