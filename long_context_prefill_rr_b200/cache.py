@@ -274,7 +274,8 @@ class PagedCache:
 
     weight, order and seen come together; a cache that has them can be evicted from. The tensors'
     contents may change between calls, the tensors themselves stay (the object holds their
-    addresses). The object owns its workspace: its calls must not overlap on the GPU.
+    addresses). The object owns its workspace: its calls must not overlap on the GPU, and it has to
+    live until they are done on the GPU.
     """
 
     def __init__(self, k, v, page_table, lengths, *, heads_q, softmax_scale=-1.0, weight=None,

@@ -118,7 +118,11 @@ rra_status resolve_sizes(const rra_cache *s, CacheView *c) {
   return RRA_OK;
 }
 
-rra_view bytes(const rra_view &v) { return {v.data, v.batch * 2, v.head * 2, v.token * 2}; }
+// A view as the kernels take it: strides in bytes, 0 for a dimension of one place (whatever was given).
+rra_view bytes(const rra_view &v, int batch, int heads, int tokens) {
+  return {v.data, batch > 1 ? v.batch * 2 : 0, heads > 1 ? v.head * 2 : 0,
+          tokens > 1 ? v.token * 2 : 0};
+}
 
 // A view that is read: aligned rows, strides of 0 allowed.
 bool readable(const rra_view &v, int batch, int heads, int tokens) {
@@ -162,9 +166,10 @@ rra_status resolve_cache(const rra_cache *s, CacheView *c) {
   if (tracked != (s->order != nullptr) || tracked != (s->seen != nullptr) ||
       !aligned4(s->weight) || !aligned4(s->order) || !aligned4(s->seen))
     return RRA_ERR_INVALID_ARG;
-  c->page_bytes = s->page_stride * 2;
-  c->head_bytes = s->head_stride * 2;
-  c->entry_bytes = s->entry_stride * 2;
+  const rra_view strides = bytes(rows, s->num_pages, s->heads_kv, s->page_size);
+  c->page_bytes = strides.batch;
+  c->head_bytes = strides.head;
+  c->entry_bytes = strides.token;
   c->table_stride = s->batch > 1 ? s->table_stride : 0;
   c->k = static_cast<uint8_t *>(s->k);
   c->v = static_cast<uint8_t *>(s->v);
@@ -225,12 +230,14 @@ rra_status resolve_tokens(const rra_rope *r, const rra_tokens *t, rra::RopeParam
   p->heads = (hq ? t->heads_q : 0) + (hk ? t->heads_kv : 0) + (hv ? t->heads_kv : 0);
   p->pos = t->positions;
   const rra_view none = {nullptr, 0, 0, 0};
-  p->q = hq ? bytes(t->q) : none;
-  p->k = hk ? bytes(t->k) : none;
-  p->v = hv ? bytes(t->v) : none;
-  p->qo = bytes(t->q_out);
-  p->ko = bytes(t->k_out);
-  p->vo = bytes(t->v_out);
+  auto q_view = [&](const rra_view &v) { return bytes(v, t->batch, t->heads_q, t->tokens); };
+  auto kv_view = [&](const rra_view &v) { return bytes(v, t->batch, t->heads_kv, t->tokens); };
+  p->q = hq ? q_view(t->q) : none;
+  p->k = hk ? kv_view(t->k) : none;
+  p->v = hv ? kv_view(t->v) : none;
+  p->qo = q_view(t->q_out);
+  p->ko = kv_view(t->k_out);
+  p->vo = kv_view(t->v_out);
   std::copy(r->turn, r->turn + RRA_ROPE_MAX_PAIRS, p->turn);
   std::copy(r->axis, r->axis + RRA_ROPE_MAX_PAIRS, p->axis);
   for (int i = 0; i < r->rotary_dim / 2; ++i)
@@ -354,10 +361,12 @@ rra_status rra_cache_decode(const rra_cache *cache, const rra_view *q, const rra
   if (s != RRA_OK) return s;
   p.q = static_cast<const uint8_t *>(q->data);
   p.out = static_cast<uint8_t *>(out->data);
-  p.q_batch = q->batch * 2;
-  p.q_head = q->head * 2;
-  p.o_batch = out->batch * 2;
-  p.o_head = out->head * 2;
+  const rra_view qs = bytes(*q, cache->batch, cache->heads_q, 1);
+  const rra_view os = bytes(*out, cache->batch, cache->heads_q, 1);
+  p.q_batch = qs.batch;
+  p.q_head = qs.head;
+  p.o_batch = os.batch;
+  p.o_head = os.head;
   p.lse = lse;
   const float scale = cache->softmax_scale > 0.f
                           ? cache->softmax_scale

@@ -467,6 +467,25 @@ def test_append_past_the_table_and_bad_pages(cuda_device):
         c.check()
 
 
+def test_strides_of_single_places_do_not_count(cuda_device):
+    """One head, one page or one entry per page: the stride that goes with it may be anything."""
+    p = Paged([5, 9], 2, 1, 64, 1, seed=27)
+    table, x = cache.RopeTable(64), randn((2, 1, 1, 64), BF, 28)
+    pos = torch.zeros(1, 2, 1, dtype=torch.int32, device="cuda")
+    p.cache.lengths.copy_(ints([4, 8]))
+    p.cache.raw.head_stride = p.cache.raw.entry_stride = -7
+    out = torch.zeros_like(x)
+    view = (x.data_ptr(), 64, -3, -5)
+    tokens = cache._pack_tokens(2, 0, 1, 1, 0, pos.data_ptr(), 0, 1, 0, *(0,) * 4, *view, *view,
+                                *(0,) * 4, out.data_ptr(), 64, -3, -5, *(0,) * 4)
+    stream = torch.cuda.current_stream().cuda_stream
+    assert native.load().rra_cache_append(p.cache._ref, table._ref, tokens, None, 1, stream) == 0
+    assert p.lens.tolist() == [5, 9] and torch.equal(out, x)      # position 0 turns nothing
+    for b, e in ((0, 4), (1, 8)):
+        assert torch.equal(p.v[p.table[b, e].long(), 0, 0], x[b, 0, 0])
+    run_decode(p)
+
+
 def test_append_refusals(cuda_device):
     p = Paged([32], 2, 1, 64, 16, seed=25)
     x, pos = randn((1, 1, 4, 64), BF, 26), torch.zeros(1, 1, 4, dtype=torch.int32, device="cuda")
