@@ -13,13 +13,14 @@
 //           budget moves one row per head, not the cache.
 //
 // Bound: 8 bytes (weight, ordinal) per entry and head read, and the moved rows read and written. Measured
-// (8 KV heads of 128, bf16): 32 sequences one entry over 2048, select 12 us and move 5; one of 128K cut to
-// 16K, 26 and 24 (the bytes take 17); eight of 32K cut to 8K, 36 and 75 (62). The move runs near the copy
-// rate; select is bound by its chain of dependent steps: length, page, weight, four digits and the ranks of
-// the lists, each with a barrier of the block or cluster. Taking the entries four at a time halved its
-// instructions and saved 2 us of 28; digits found bit by bit took 760 cycles a bit against 1700 a digit; keys
-// in registers, unrolled, were no faster than these rolled loops (each stretch of new instructions has to be
-// fetched first); a third launch that marked the pages beforehand cost 3 us.
+// from cold caches (8 KV heads of 128, bf16): 32 sequences one entry over 2048, select 11 us and move 6; one
+// of 128K cut to 16K, 25 and 24 (the bytes take 18); eight of 32K cut to 8K, 26 and 74 (62). The move runs
+// at 75-83% of the copy rate; select is bound by its chain of dependent steps: length, page, weight, four
+// digits and the ranks of the lists, each with a barrier of the block or cluster. Taking the entries four
+// at a time halved its instructions and saved 2 us of 28; digits found bit by bit took 760 cycles a bit
+// against 1700 a digit; keys in registers, unrolled, were no faster than these rolled loops (each stretch
+// of new instructions has to be fetched first); a third launch that marked the pages beforehand cost 3 us;
+// dealing the moves out over warps that stay made the move slower (52 us against 44, five ragged sequences).
 #include <cooperative_groups.h>
 
 #include <limits.h>
@@ -445,10 +446,11 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
 // A warp takes kFlight moves (twice as many for head_dim 64, whose two rows fill half a warp) of a
 // (sequence, KV head) at a time: as many lanes move a weight and an ordinal each, then the warp copies the
 // rows, all loads before the first store.
-constexpr int kFlight = 8;
+constexpr int kFlight = 4;
+constexpr int kMoveBlocks = 4;     // blocks that share an SM
 
 template <int D>
-__global__ void __launch_bounds__(kMoveWarps * 32, 3)
+__global__ void __launch_bounds__(kMoveWarps * 32, kMoveBlocks)
     evict_move_kernel(const __grid_constant__ EvictParams p, int parts) {
   constexpr int VECS = D / 8;                  // 16-byte vectors of a row
   constexpr int PER = 32 / (2 * VECS);         // moves whose key and value rows fill a warp: 1 or 2
@@ -560,11 +562,14 @@ cudaError_t launch_evict(const EvictParams &p, int num_sms, cudaStream_t stream)
     e = launch_dependent(kern, dim3(static_cast<unsigned>(items) * ranks), threads, room * 4, ranks,
                          stream, p, room);
   if (e != cudaSuccess) return e;
-  // Blocks of the move kernel: as many as its longest possible lists can use, up to twelve per SM, so that
-  // the hardware evens out items with many moves and with none.
+  // Blocks of the move kernel: as many as its longest possible lists can use, up to two rounds of those that fit,
+  // so that the hardware evens out items with many moves and with none. Whole passes over five ragged sequences of
+  // up to 128K, and over eight of 32K: one round 83 and 113 us, two 81 and 114, five 81 and 118; eight moves in
+  // flight and three blocks per SM 85 and 124.
   const int64_t most = std::max(1, std::min(p.budget, c.cap - p.budget));
   const int per_block = kMoveWarps * kFlight * (c.d == 128 ? 1 : 2);
-  const int64_t blocks = std::min<int64_t>(num_sms * 12, items * ((most + per_block - 1) / per_block));
+  const int64_t blocks =
+      std::min<int64_t>(num_sms * kMoveBlocks * 2, items * ((most + per_block - 1) / per_block));
   const dim3 grid(static_cast<unsigned>(blocks));
   const int parts = static_cast<int>(std::max<int64_t>(1, blocks * kMoveWarps / items));
   return c.d == 128 ? launch_dependent(evict_move_kernel<128>, grid, kMoveWarps * 32, 0, 1, stream,
