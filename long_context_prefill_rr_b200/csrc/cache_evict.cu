@@ -83,7 +83,8 @@ __device__ __forceinline__ void claim_pages(const EvictParams &p, int b, const C
         (static_cast<unsigned long long>(cut.tag) << 32) | static_cast<unsigned>(b);
     const unsigned long long was = atomicExch(p.owner + pg, me);
     if (static_cast<uint32_t>(was >> 32) == cut.tag) {
-      const int other = static_cast<int>(static_cast<uint32_t>(was));
+      // (a sequence of this cache, unless the workspace was laid out for another and not zero-filled since)
+      const int other = static_cast<int>(min(static_cast<uint32_t>(was), c.batch - 1u));
       p.skip[b] = cut.tag;
       p.skip[other] = cut.tag;
       // no mistake as long as neither of them is to be cut
