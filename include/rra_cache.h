@@ -127,7 +127,8 @@ size_t rra_cache_workspace_bytes(const rra_cache *cache);
  * int32 [batch] with the tokens of each sequence that are real, or NULL for all; padding (t >=
  * new_len[b]) is neither read nor written. Tracked caches get weight 0 and ordinal seen[b] + t.
  * advance != 0 adds the new tokens to len and seen; layers that share them advance with the last
- * one. Entries past the page table are dropped and flagged. */
+ * one. Entries past the page table are dropped and flagged. Sequences may share pages as long as no
+ * two tokens of a call fall on the same row (of those one is kept, any). */
 rra_status rra_cache_append(const rra_cache *cache, const rra_rope *rope,
                             const rra_tokens *tokens, const int32_t *new_len, int advance,
                             rra_stream_t stream);
