@@ -128,7 +128,7 @@ size_t rra_cache_workspace_bytes(const rra_cache *cache);
  * new_len[b]) is neither read nor written. Tracked caches get weight 0 and ordinal seen[b] + t.
  * advance != 0 adds the new tokens to len and seen; layers that share them advance with the last
  * one. Entries past the page table are dropped and flagged. Sequences may share pages as long as no
- * two tokens of a call fall on the same row (of those one is kept, any). */
+ * two tokens of a call fall on the same row (theirs would mix). */
 rra_status rra_cache_append(const rra_cache *cache, const rra_rope *rope,
                             const rra_tokens *tokens, const int32_t *new_len, int advance,
                             rra_stream_t stream);
