@@ -62,11 +62,15 @@ __device__ __forceinline__ uint4 ld_stream(const void *p) {
   return v;
 }
 
+// kRaise: decode multiplies the softmax weights, which are 1 at most, by 2^kRaise before it rounds them to
+// the element type. fp16 has a smallest step of 2^-24: raised by 15 (32768 is still below its largest
+// value) a weight keeps 2^-40 of the largest one.
 template <class T>
 struct Elem;
 
 template <>
 struct Elem<__nv_bfloat16> {
+  static constexpr int kRaise = 0;
   static __device__ __forceinline__ float2 unpack(uint32_t u) {
     return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
   }
@@ -87,6 +91,7 @@ struct Elem<__nv_bfloat16> {
 
 template <>
 struct Elem<__half> {
+  static constexpr int kRaise = 15;
   static __device__ __forceinline__ float2 unpack(uint32_t u) {
     return __half22float2(*reinterpret_cast<const __half2 *>(&u));
   }

@@ -19,8 +19,10 @@
 // k-steps; the columns of p.v may be permuted as well, so a thread takes 16 bytes of each of four
 // value rows and pairs up the rows' elements. The 8 query heads fill rows 0-7 of the 16-row MMA
 // tile. Rows 8-15 of the p.v product hold the low parts of the same weights (p = hi + lo, both 16-bit),
-// so the weights keep twice the bits of the element type at no cost. With more than 8 heads to a KV head
-// rows 8-15 hold 8 more of them, and the low parts take a second product.
+// so the weights keep twice the bits of the element type at no cost: 2^-17 of themselves in bf16; in fp16
+// 2^-22 of themselves or 2^-40 of the largest weight, whichever is more, because they are raised by 2^15
+// first (unraised, entries 17.3 nats below an attention sink were 0 here and counted in the denominator).
+// With more than 8 heads to a KV head rows 8-15 hold 8 more of them, and the low parts take a second product.
 //
 // Measured on the way (128K entries, 32 / 8 heads of 128, 537 MB; the copy rate gives 82 us): fragments
 // loaded straight into registers 107 us (64-byte requests, 56% of the load pipe's wavefronts); the
@@ -83,6 +85,9 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
 // long as logits, weights and value rows agree; this one puts the rows that a read touches together
 // (columns 2 t, 2 t + 1 of the keys; the four values of t for the value rows) into different banks.
 __device__ __forceinline__ int entry_of(int t, int e) { return e ? 4 + ((t + 2) & 3) : t; }
+
+// 2^n for -126 < n < 127.
+constexpr float exp2_of(int n) { return n < 0 ? exp2_of(n + 1) * 0.5f : n > 0 ? exp2_of(n - 1) * 2.f : 1.f; }
 
 // Where a CTA's run of units starts.
 struct Cursor {
@@ -185,6 +190,9 @@ __global__ void __launch_bounds__(kThreads, decode_ctas(D))
   constexpr int S = kStages;
   constexpr uint32_t PITCH = kPitch<D>, STAGE = kStageBytes<D>;
   constexpr int ROW = D + 4;        // padded row of the merge buffer
+  // The weights in the registers, their sums and the outputs are 2^RAISE times too large. The sums lose the
+  // factor when they leave the registers, the outputs when they are divided by them.
+  constexpr float RAISE = Elem<T>::kRaise, LOWER = exp2_of(-Elem<T>::kRaise);
   static_assert(S <= 4 && S * STAGE >= TILE * ROW * 4, "exist masks, merge buffer");
   extern __shared__ __align__(128) uint8_t s_ring[];
   __shared__ int s_scan[20];
@@ -352,7 +360,9 @@ __global__ void __launch_bounds__(kThreads, decode_ctas(D))
         const float base = m_run[h] == -INFINITY ? 0.f : m_run[h];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float w0 = fast_exp2(x[h][2 * i] - base), w1 = fast_exp2(x[h][2 * i + 1] - base);
+          // (the difference is rounded before the factor is added: it is never above 0)
+          const float w0 = fast_exp2(x[h][2 * i] - base + RAISE);
+          const float w1 = fast_exp2(x[h][2 * i + 1] - base + RAISE);
           l_run[h] += w0 + w1;
           hi[h][i] = Elem<T>::pack(w0, w1);
           const float2 f = Elem<T>::unpack(hi[h][i]);
@@ -394,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, decode_ctas(D))
       l_run[h] += __shfl_xor_sync(0xffffffffu, l_run[h], 2);
       if (t == 0) {
         s_m[warp][r + 8 * h] = m_run[h];
-        s_l[warp][r + 8 * h] = l_run[h];
+        s_l[warp][r + 8 * h] = l_run[h] * LOWER;
       }
     }
     // the thread's columns 2t and 2t + 1 of the permuted tiles are dimensions 16t .. 16t + 15 of
@@ -442,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, decode_ctas(D))
         o.w += f * x.w;
       }
       if (whole) {
-        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);   // NaN stays
+        const float inv = l > 0.f ? LOWER / l : (l == 0.f ? 0.f : l);   // NaN stays
         *reinterpret_cast<uint2 *>(p.out + b * p.o_batch + (h0 + row) * p.o_head + col * 2) =
             make_uint2(Elem<T>::pack(o.x * inv, o.y * inv), Elem<T>::pack(o.z * inv, o.w * inv));
         if (col == 0) {
@@ -487,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, decode_ctas(D))
             o.z = o.z * fa + x.z * fb;
             o.w = o.w * fa + x.w * fb;
           }
-          const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+          const float inv = l > 0.f ? LOWER / l : (l == 0.f ? 0.f : l);
           *reinterpret_cast<uint2 *>(p.out + b * p.o_batch + (h0 + row) * p.o_head + col * 2) =
               make_uint2(Elem<T>::pack(o.x * inv, o.y * inv),
                          Elem<T>::pack(o.z * inv, o.w * inv));
