@@ -1,5 +1,5 @@
 """Decode attention where the values or the weights are out of the ordinary: weights far below the
-largest one. Against the definition in 64 bits; the tolerances of each test are derived beside it.
+largest one, values at the end of the type's range. Against the definition in 64 bits; the tolerances of each test are derived beside it.
 """
 import math
 
@@ -57,4 +57,31 @@ def test_decode_long_tail_behind_a_sink(cuda_device, dtype, nats, group, d):
     # 2^-18 of the tail's share, the sums as above, the logarithm and the change of base
     assert float((lse.double().cpu() - nats - math.log1p(tail)).abs().max()) <= \
         2.0 ** -18 + 2.0 ** -14 + 2.0 ** -21 * (1 + nats)
+    c.check()
+
+
+# ------------------------------------------------------------------------------------- large values
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("group,d", [(1, 128), (12, 64)])
+@pytest.mark.parametrize("n", [3, 500, 20000])
+def test_decode_values_at_the_end_of_the_range(cuda_device, dtype, group, d, n):
+    """The type's largest values, of one sign and of both: their sums pass fp32's range in bf16, their means
+    do not. All keys are 0, so all weights are equal (1 / n, exact but for the reciprocal of n, 2^-23);
+    each truncated addition is off by 2^-23 of the sum of the magnitudes, and a warp makes at most
+    n / 16 + 1 of them, the joins 300 more. What is past the largest value by less than half a step rounds
+    to it, and the mean of one value cannot be more."""
+    hkv, ps, top = 2, 20, torch.finfo(dtype).max
+    pages = -(-n // ps)
+    k = torch.zeros(pages, hkv, ps, d, dtype=dtype, device="cuda")
+    v = torch.full((pages, hkv, ps, d), top, dtype=dtype, device="cuda")
+    v[..., 1::4] = -top
+    g = torch.Generator(device="cuda").manual_seed(n)
+    v[..., 2::4] *= torch.randint(0, 2, v[..., 2::4].shape, generator=g, device="cuda").to(dtype) * 2 - 1
+    c = cache.PagedCache(k, v, ints([list(range(pages))]), ints([n]), heads_q=hkv * group)
+    out = c.decode(torch.ones(1, hkv * group, d, dtype=dtype, device="cuda"))
+    ref = v.transpose(0, 1).reshape(hkv, pages * ps, d)[:, :n].double().mean(1)
+    ref = ref.repeat_interleave(group, 0)[None]
+    tol = half_step(dtype) * ref.abs() + top * ((n / 16 + 301) * 2.0 ** -23 + 2.0 ** -22)
+    assert out.isfinite().all()
+    assert ((out.double() - ref).abs() <= tol).all()
     c.check()
