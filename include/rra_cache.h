@@ -136,8 +136,11 @@ rra_status rra_cache_append(const rra_cache *cache, const rra_rope *rope,
 /* out[b, h] = sum over the entries e < len[b] of softmax(softmax_scale q_h . k_e) v_e; lse[b, h]
  * (fp32 [batch, heads_q], may be NULL) the natural logarithm of the softmax's denominator. q and
  * out are views with one token (their token stride is not used); out may be q. A sequence without
- * entries gets out 0 and lse -inf. A logit of -inf counts as absent. Logits, sums and outputs are
- * held in fp32 and rounded once, to the element type. add_weight != 0 (tracked caches)
+ * entries gets out 0 and lse -inf. A logit of -inf counts as absent, whatever its value. Any other
+ * entry has a weight above 0, however small: an infinite value makes its output infinite, a NaN or
+ * infinities of both signs make it NaN. A logit of +inf or NaN makes its head's out and lse NaN (and
+ * the weights that the head gives, with add_weight). Logits, sums and outputs are held in fp32 and
+ * rounded once, to the element type. add_weight != 0 (tracked caches)
  * adds to the weight of every entry and KV head the softmax weights that the KV head's query heads
  * gave it. Rows of page_table may share pages here; with add_weight a shared entry then gets
  * the sum of its rows, added in no fixed order. Otherwise equal calls give equal bits. */

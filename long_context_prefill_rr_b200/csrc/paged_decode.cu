@@ -35,6 +35,7 @@
 // two passes of 8 took 106 (4 x 40000 entries, 328 MB).
 // A call of 1000 entries takes 8 us, 2 of them the join of 16 pieces; reading eight pieces at a time
 // there made it slower (10: the longer code has to be fetched).
+#include <float.h>
 #include <math.h>
 
 #include "cache_device.cuh"
@@ -179,6 +180,83 @@ __device__ __forceinline__ void next_sequence(const CacheView &c, int items, Cur
     cur->len = cache_len(c, cur->b);
   } while (cur->len == 0 && cur->b + 1 < c.batch);
   cur->units = units_of(cur->len);
+}
+
+// One query head's sums over a warp's entries of a piece, again: where values that are infinite or NaN meet
+// weights of 0 (logits of -inf) or the low parts of others, the matrix product has 0 * inf. Here an entry
+// without a weight is left out, and the other values that are not finite are noted for each dimension
+// apart from the sum. A lane takes D / 32 dimensions of eight entries at a time, for the heads and warps that
+// it happens to: 128K entries, 32 / 8 heads of 128, take 1.1 ms with an infinity under every KV head and 1.6 with
+// nothing but NaN, against 90 us. Code of its own, because the same within the loop below cost every call
+// 0.4 us, and 2 of 93 (32 sequences of up to 8K).
+template <class T, int D>
+__device__ __noinline__ void add_up_again(const DecodeParams &p, int b, int kv_head, int head, int e0,
+                                          int key1, float *out, float *max_out, float *sum_out) {
+  constexpr int PER = D / 32, BATCH = 8;   // BATCH: entries in flight
+  const CacheView &c = p.c;
+  const int lane = threadIdx.x & 31;
+  auto read = [&](int64_t at, const uint8_t *base, float (&x)[PER]) {
+#pragma unroll
+    for (int i = 0; i < PER; i += 2) {
+      const int byte = (lane * PER + i) * 2;
+      const float2 y = Elem<T>::unpack(at < 0 ? 0u : *reinterpret_cast<const uint32_t *>(base + at + byte));
+      x[i] = y.x, x[i + 1] = y.y;
+    }
+  };
+  float q[PER], acc[PER] = {}, top = -INFINITY, sum = 0.f;
+  read(b * p.q_batch + head * p.q_head, p.q, q);
+  uint32_t plus = 0, minus = 0;        // dimensions with a value of +inf or NaN, and of -inf or NaN
+#pragma unroll 1
+  for (int kb = e0; kb < key1; kb += kDecodeUnit) {
+    int64_t mine = -1;
+    if (kb + (lane & 15) < key1) {
+      int slot, off;
+      split_entry(c, kb + (lane & 15), slot, off);
+      const int pg = page_at(c, b, slot);
+      if (pg >= 0) mine = pg * c.page_bytes + off * c.entry_bytes;
+    }
+#pragma unroll 1
+    for (int j = 0; j < 16; j += BATCH) {
+      float x[BATCH], v[BATCH][PER];
+#pragma unroll
+      for (int n = 0; n < BATCH; ++n) {
+        const int64_t at = __shfl_sync(0xffffffffu, mine, j + n);
+        float k[PER];
+        read(at, c.k + kv_head * c.head_bytes, k);
+        read(at, c.v + kv_head * c.head_bytes, v[n]);
+        x[n] = 0.f;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) x[n] = fmaf(q[i], k[i], x[n]);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int n = 0; n < BATCH; ++n) x[n] += __shfl_xor_sync(0xffffffffu, x[n], o);
+#pragma unroll
+      for (int n = 0; n < BATCH; ++n) {
+        x[n] *= p.scale_log2;          // the same in all lanes
+        if (x[n] == -INFINITY || __shfl_sync(0xffffffffu, mine, j + n) < 0) continue;
+        const float top_new = fmaxf(top, x[n]), alpha = exp2f(top - top_new), w = exp2f(x[n] - top_new);
+        top = top_new;
+        sum = sum * alpha + w;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          const float y = v[n][i];
+          const bool finite = fabsf(y) < INFINITY;
+          acc[i] = acc[i] * alpha + (finite ? w * exp2_of(Elem<T>::kRaise) * y : 0.f);
+          if (!finite && !(y < 0.f)) plus |= 1u << i;
+          if (!finite && !(y > 0.f)) minus |= 1u << i;
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    if ((plus >> i) & 1u) acc[i] += INFINITY;
+    if ((minus >> i) & 1u) acc[i] -= INFINITY;
+    out[lane * PER + i] = acc[i];
+  }
+  if (lane == 0) *max_out = top, *sum_out = sum;
 }
 
 // TILE: query heads of a KV head that a warp carries, 8 or 16.
@@ -398,6 +476,13 @@ __global__ void __launch_bounds__(kThreads, decode_ctas(D))
     copy_wait<0>();
     __syncwarp();
 
+    // heads with a sum that is not finite: sums and products with 0 tell
+    float not_finite[HT] = {};
+#pragma unroll
+    for (int i = 0; i < NH * 8; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) not_finite[q / 2 * (HT - 1)] += acc[i][q] * 0.f;
+
     // ---- the warps' results meet in shared memory
 #pragma unroll
     for (int h = 0; h < HT; ++h) {
@@ -427,6 +512,18 @@ __global__ void __launch_bounds__(kThreads, decode_ctas(D))
             *reinterpret_cast<float4 *>(s_o(warp) + (r + 8 * w) * ROW + h * 64 + t * 16 + q * 8 + e) =
                 make_float4(y[0], y[1], y[2], y[3]);
           }
+    uint32_t again[HT];
+#pragma unroll
+    for (int h = 0; h < HT; ++h)       // (a denominator of NaN stays)
+      again[h] = __ballot_sync(0xffffffffu, r + 8 * h < rows && not_finite[h] != 0.f && l_run[h] == l_run[h]);
+    if (__builtin_expect((again[0] | again[HT - 1]) != 0u, 0)) {
+      __syncwarp();
+#pragma unroll 1
+      for (int row = 0; row < rows; ++row)
+        if (((row < 8 ? again[0] : again[HT - 1]) >> (row & 7) * 4) & 0xfu)
+          add_up_again<T, D>(p, b, head, h0 + row, unit0 * kDecodeUnit + warp * 16, key1,
+                             s_o(warp) + row * ROW, &s_m[warp][row], &s_l[warp][row]);
+    }
     __syncthreads();
 
     const int first_unit = cur.start + m * cur.units;
@@ -442,15 +539,16 @@ __global__ void __launch_bounds__(kThreads, decode_ctas(D))
       const float base = mt == -INFINITY ? 0.f : mt;
       float l = 0.f;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      // factors of at least FLT_MIN (2^-126, nothing beside the largest one, 1) leave infinities as they are
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float f = exp2f(s_m[w][row] - base);
+        const float f = exp2f(s_m[w][row] - base), g = fmaxf(f, FLT_MIN);
         const float4 x = *reinterpret_cast<const float4 *>(s_o(w) + row * ROW + col);
         l += f * s_l[w][row];
-        o.x += f * x.x;
-        o.y += f * x.y;
-        o.z += f * x.z;
-        o.w += f * x.w;
+        o.x += g * x.x;
+        o.y += g * x.y;
+        o.z += g * x.z;
+        o.w += g * x.w;
       }
       if (whole) {
         const float inv = l > 0.f ? LOWER / l : (l == 0.f ? 0.f : l);   // NaN stays
@@ -491,12 +589,13 @@ __global__ void __launch_bounds__(kThreads, decode_ctas(D))
             const float mn = fmaxf(mt, y.x);
             const float base = mn == -INFINITY ? 0.f : mn;
             const float fa = exp2f(mt - base), fb = exp2f(y.x - base);
+            const float ga = fmaxf(fa, FLT_MIN), gb = fmaxf(fb, FLT_MIN);
             mt = mn;
             l = l * fa + y.y * fb;
-            o.x = o.x * fa + x.x * fb;
-            o.y = o.y * fa + x.y * fb;
-            o.z = o.z * fa + x.z * fb;
-            o.w = o.w * fa + x.w * fb;
+            o.x = o.x * ga + x.x * gb;
+            o.y = o.y * ga + x.y * gb;
+            o.z = o.z * ga + x.z * gb;
+            o.w = o.w * ga + x.w * gb;
           }
           const float inv = l > 0.f ? LOWER / l : (l == 0.f ? 0.f : l);
           *reinterpret_cast<uint2 *>(p.out + b * p.o_batch + (h0 + row) * p.o_head + col * 2) =

@@ -1,5 +1,6 @@
 """Decode attention where the values or the weights are out of the ordinary: weights far below the
-largest one, values at the end of the type's range. Against the definition in 64 bits; the tolerances of each test are derived beside it.
+largest one, values at the end of the type's range,
+infinities and NaN among the values. Against the definition in 64 bits; the tolerances of each test are derived beside it.
 """
 import math
 
@@ -85,3 +86,121 @@ def test_decode_values_at_the_end_of_the_range(cuda_device, dtype, group, d, n):
     assert out.isfinite().all()
     assert ((out.double() - ref).abs() <= tol).all()
     c.check()
+
+
+# --------------------------------------------------------------------- values that are not finite
+def cached(n, hkv, d, ps, dtype, seed):
+    """A cache of one sequence whose pages are in order: the contiguous keys and values behind its pages'
+    views are k, v [hkv, n, d]."""
+    pages = -(-n // ps)
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    k, v = (torch.randn(hkv, pages * ps, d, generator=g, device="cuda").to(dtype) for _ in range(2))
+    def paged(x):
+        return x.view(hkv, pages, ps, d).transpose(0, 1)
+    return k, v, lambda hq, **kw: cache.PagedCache(paged(k), paged(v), ints([list(range(pages))]), ints([n]),
+                                                   heads_q=hq, **kw)
+
+
+def by_definition(q, k, v, n, scale):
+    """out, lse [hq, ...] in 64 bits; entries with a logit of -inf are left out."""
+    hq, hkv = q.shape[0], k.shape[0]
+    q, k, v = (x.double().cpu().numpy() for x in (q, k[:, :n], v[:, :n]))
+    out, lse = np.zeros(q.shape), np.full(hq, -math.inf)
+    reach = np.zeros(hq)
+    with np.errstate(invalid="ignore", over="ignore"):
+        for h in range(hq):
+            s = k[h // (hq // hkv)] @ q[h] * scale
+            live = s > -math.inf
+            if live.any():
+                top = s[live].max()
+                p = np.exp(s[live] - top)
+                # no weight is 0, so that an infinite value is infinite behind any of them
+                p = np.maximum(p / p.sum(), 1e-300)
+                out[h] = (p[:, None] * v[h // (hq // hkv)][live]).sum(0)
+                lse[h] = top + math.log(np.exp(s[live] - top).sum())
+                reach[h] = (np.abs(k[h // (hq // hkv)][live]) @ np.abs(q[h])).max() * scale
+    return out, lse, reach
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("group,d", [(4, 64), (5, 128), (11, 64), (16, 128)])
+@pytest.mark.parametrize("n,ps", [(1, 16), (90, 7), (3001, 16), (40000, 64)])
+def test_decode_values_that_are_not_finite(cuda_device, dtype, group, d, n, ps):
+    """Infinities and NaN among the values, in entries that have a weight (some of them e^-200 of the
+    largest) and in entries whose logit is -inf, which do not count. The other outputs as always: a logit is
+    off by delta = (d + 4) 2^-23 scale sum |q k|, a weight by that and 2^-21, its two parts by 2^-17; the
+    output by twice their sum of max |v|, and half a step."""
+    hkv = 2
+    k, v, make = cached(n, hkv, d, ps, dtype, n + d)
+    scale = 1 / math.sqrt(d)
+    q = torch.randn(hkv * group, d, generator=torch.Generator().manual_seed(n)).cuda().to(dtype)
+    q[:, 0], k[:, :, 0] = 1.0, 0.0
+    rng = np.random.default_rng(n + d)
+    vmax = float(v.abs().max())
+    for i in range(12 if n > 1 else 1):
+        e, h = int(rng.integers(n)), int(rng.integers(hkv))
+        v[h, e, int(rng.integers(d))] = (math.inf, -math.inf, math.nan)[i % 3]
+        if i % 4 == 1:
+            k[h, e, 0] = -200.0 * math.sqrt(d)                      # a weight of e^-200
+    if n > 1:
+        v[0, n // 2, 5], v[0, n // 3, 5] = math.inf, -math.inf      # NaN together
+        v[1, n // 2, 6], v[1, n // 3, 6] = -math.inf, -math.inf
+        gone = rng.choice(n, size=n // 8, replace=False)            # no weight at all
+        gone = gone[(gone != n // 2) & (gone != n // 3)]
+        k[:, gone, 0] = -math.inf
+        v[:, gone[::2], 7:9] = math.nan
+        v[:, gone[1::2], 8:10] = math.inf
+    # and behind the last entry
+    k[:, n:], v[:, n:] = math.nan, math.nan
+    c = make(hkv * group)
+    lse = torch.zeros(1, hkv * group, device="cuda")
+    out = c.decode(q[None], lse=lse)[0].double().cpu().numpy()
+    ref, rlse, reach = by_definition(q, k, v, n, scale)
+    assert np.isnan(ref).any() == (n > 1) and np.isinf(ref).any() and (n == 1 or (~np.isfinite(ref)).sum() < ref.size / 2)
+    assert np.array_equal(np.isnan(out), np.isnan(ref))
+    assert np.array_equal(out[np.isinf(ref)], ref[np.isinf(ref)])
+    ok = np.isfinite(ref)
+    delta = (d + 4) * 2.0 ** -23 * reach
+    tol = half_step(dtype) * np.abs(ref) + (2 * vmax * (delta + 2.0 ** -17 + 2.0 ** -20))[:, None] + \
+        (2.0 ** -25 if dtype == HF else 0)
+    assert (np.abs(out[ok] - ref[ok]) <= tol[ok]).all()
+    assert (np.abs(lse[0].double().cpu().numpy() - rlse) <=
+            delta + 2.0 ** -21 * (1 + np.abs(rlse))).all()
+    c.check()
+
+
+def test_decode_nothing_left_but_values_that_are_not_finite(cuda_device):
+    k, v, make = cached(50, 2, 64, 16, BF, 1)
+    k[:], v[:] = -math.inf, math.nan
+    q = torch.ones(1, 4, 64, dtype=BF, device="cuda")
+    lse = torch.zeros(1, 4, device="cuda")
+    assert not make(4).decode(q, lse=lse).any() and (lse == -math.inf).all()
+    k[:, 20] = 0.0
+    v[:, 20] = 3.0
+    assert (make(4).decode(q, lse=lse) == 3).all() and not lse.any()
+    v[0, 20] = math.inf
+    out = make(4).decode(q, lse=lse)[0]
+    assert (out[:2] == math.inf).all() and (out[2:] == 3).all() and not lse.any()
+
+
+@pytest.mark.parametrize("bad", [math.inf, math.nan])
+def test_decode_logits_that_are_not_finite(cuda_device, bad):
+    """A logit of +inf or NaN: NaN for its head alone, also where its values are infinite."""
+    k, v, make = cached(300, 1, 64, 16, HF, 2)
+    k[0, :, :2], k[0, 100, 0] = 0.0, bad
+    v[0, 100, 3], v[0, 200, 4] = math.inf, math.inf
+    q = torch.randn(1, 3, 64, generator=torch.Generator().manual_seed(3)).to(HF).cuda()
+    q[0, :, 0] = torch.tensor([1.0, 2.0, -1.0], dtype=HF)
+    shape = (19, 1, 16)
+    weight = torch.zeros(shape, device="cuda")
+    c = make(3, weight=weight, order=torch.zeros(shape, dtype=torch.int32, device="cuda"),
+             seen=ints([300]))
+    lse = torch.zeros(1, 3, device="cuda")
+    out = c.decode(q, lse=lse, add_weight=True)
+    assert out[0, :2].isnan().all() and lse[0, :2].isnan().all()
+    if bad == math.inf:                    # the third head's logit is -inf: absent, with its value
+        assert out[0, 2, 4] == math.inf and out[0, 2, 3].isfinite() and lse[0, 2].isfinite()
+        assert out[0, 2].isfinite().sum() == 63
+    else:
+        assert out[0, 2].isnan().all()
+    assert weight.view(-1)[:300].isnan().all()
