@@ -8,7 +8,9 @@ before and behind the prefill of ``native``.
 
 Like ``native`` this is argument marshalling only, on torch CUDA tensors; every operator runs in the
 library's kernels. Calls run on the tensors' device, on its current stream unless ``stream`` is
-given, do not synchronise and are not recorded by autograd.
+given, do not synchronise and are not recorded by autograd. With ``stream`` the caller orders the
+streams: the call does not wait for the current stream's work on its inputs, nor the current stream for
+the outputs. Inputs and outputs may be dropped as soon as the call has returned.
 """
 from __future__ import annotations
 
@@ -125,10 +127,23 @@ def _raw_stream(stream, device):
 
 
 def _new(shape, dtype, device, stream):
-    x = torch.empty(shape, dtype=dtype, device=device)
-    if stream is not None:
-        x.record_stream(stream)      # torch made it for the current stream
+    """An output, allocated for the stream that writes it: a block of the current stream's may still be in
+    use there by what was freed, and nothing makes ``stream`` wait for that."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        x = torch.empty(shape, dtype=dtype, device=device)
+    x.record_stream(torch.cuda.current_stream(device))    # where the caller reads it
     return x
+
+
+def _used(stream, *tensors):
+    """Keeps the blocks of a call's tensors until ``stream`` is done with them, also where the caller drops
+    the tensors before."""
+    if stream is not None:
+        for x in tensors:
+            if x is not None:
+                x.record_stream(stream)
 
 
 class RopeTable:
@@ -241,6 +256,7 @@ def _fill_tokens(table, positions, q, k, v, q_out, k_out, v_out, stream):
         raise ValueError("v_out is given without v")
     t = _pack_tokens(b, heads_q, heads_kv, n, code, positions.data_ptr(), p0, p1, p2, *q_view,
                      *k_view, *v_view, *q_to, *k_to, *v_to)
+    _used(stream, positions, q, k, v, q_out, k_out, v_out)
     return t, device, heads_q, (q_out, k_out, v_out)
 
 
@@ -373,6 +389,7 @@ class PagedCache:
             _need(new_len, "new_len", device, torch.int32, (self.batch,))
             if not new_len.is_contiguous():
                 raise ValueError("new_len must be contiguous")
+            _used(stream, new_len)
         native._check(_call(device, self._lib.rra_cache_append, self._ref, table._ref, t,
                             None if new_len is None else new_len.data_ptr(), 1 if advance else 0,
                             _raw_stream(stream, device)), "rra_cache_append")
@@ -403,6 +420,7 @@ class PagedCache:
             at = lse.data_ptr()
         if add_weight and not self.tracked:
             raise ValueError("add_weight needs a cache with weight, order and seen")
+        _used(stream, q, out, lse)
         native._check(_call(device, self._lib.rra_cache_decode, self._ref,
                             _pack_view(q.data_ptr(), sq[0], sq[1], 0),
                             _pack_view(out.data_ptr(), so[0], so[1], 0), at,
