@@ -178,9 +178,9 @@ __global__ void __launch_bounds__(256, kBlocks)
       }
   }
   if (!CACHED) return;
-  // lengths outside the table, reported once per sequence
-  if (blockIdx.y == 0 && real && t == 0 && u == 0 &&
-      (first < 0 || static_cast<int64_t>(first) + min(new_tokens, p.tokens) > c.cap))
+  // lengths outside the table, reported once per sequence, whether it has new tokens or not
+  if (blockIdx.y == 0 && there && t == 0 && u == 0 &&
+      (first < 0 || static_cast<int64_t>(first) + max(min(new_tokens, p.tokens), 0) > c.cap))
     raise(c.status, kErrBadLength);
   if (!p.advance) return;
   // The last block to have read len and seen moves them on and resets the count.
