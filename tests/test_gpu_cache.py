@@ -3,15 +3,18 @@
 Tolerances, from the arithmetic of the kernels (eps / 2 is half a step of the element type, relative):
 
 * a rotated value x cos - y sin: half a step of the result for the final rounding, and for the
-  fp32 angle, sine, cosine, products and sum less than 2^-20 of |(x, y)|. The angle is a fraction of a
-  half turn rounded to 24 bits (2^-25 pi), sine and cosine are good to 2 ulp, each product
-  and the sum to half an ulp: 2^-23.3 + 2^-22 + 3 * 2^-24 < 2^-21. fp16 results below 2^-14 have steps
-  of 2^-24. The fp64 angle is itself off by 2^-53 |angle|.
+  fp32 angle, sine, cosine, products and sum less than 2^-20 of |(x, y)|. With u = 2^-24: the angle within its
+  quadrant is at most pi / 4; its conversion, the factor and the product are off by u of it each, and its last
+  bit is 2^-32 of a turn: 2.4 u. The series of the sine is off by 0.9 u, that of the cosine by 1.0 u for
+  roundings and 0.4 u for what is cut off (test_gpu_rope_angles.py adds it up); products and sum 2 u. In all
+  6.1 u < 2^-21. fp16 results below 2^-14 have steps of 2^-24. The fp64 angle is itself off by
+  2^-53 |angle|.
 * a logit: products of 16-bit values are exact in fp32; d of them are added in fp32, each addition
   off by at most 2^-23 (the tensor cores truncate) of the sum of the magnitudes, R = scale * sum |q_i k_i|.
   Scaling to log2 and back costs 3 roundings. delta = (d + 4) 2^-23 R bounds its absolute error.
 * a weight's relative error: delta + 2^-21 (subtraction, exp2 and the reciprocal of the sum), and
-  2^-17 for the two 16-bit parts that multiply V (bf16: (2^-9)^2, doubled). An output is a mean of V rows
+  2^-17 for the two 16-bit parts that multiply V (bf16: (2^-9)^2, doubled; fp16: (2^-12)^2, doubled, or
+  2^-40 of the largest weight). An output is a mean of V rows
   with those weights: 2 (delta + 2^-17 + 2^-20) max |v|, and half a step.
 * lse: delta + 2^-21 (1 + |lse|) for the sum, the logarithm and the change of base.
 * an accumulated weight: for each of the g heads (delta + 2^-21) of itself for the logit and as much
