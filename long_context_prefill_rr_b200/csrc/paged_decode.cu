@@ -3,7 +3,8 @@
 // softmax, one pass over K and V.
 //
 // Memory bound: 4 d bytes per entry and KV head against 4 d flop per query head, so K and V have to
-// be read once, at HBM speed, and everything else stays in registers.
+// be read once, at HBM speed, and everything else stays in registers. (More than 16 query heads to a KV
+// head read them once per 16.)
 //
 // Work. The entries of all (sequence, KV head, head tile) items are laid end to end in units of 64
 // and cut into equal runs, one per CTA, whatever the lengths are (they are read on the device, so a
@@ -58,7 +59,9 @@ constexpr uint32_t kStageBytes = 32 * kPitch<D>;
 template <int D>
 constexpr size_t kRingBytes = static_cast<size_t>(kWarps) * kStages * kStageBytes<D>;
 
-// Keys and values are read once: they leave L2 first, before the logits and pieces that are read again.
+// Keys and values leave L2 first, before the logits and pieces that are read again. That holds with more than 16
+// query heads to a KV head too, which read them once per head tile, from CTAs that do not run side by
+// side: 4 x 128K entries, 32 heads over one, take 115 us so, and 127 with rows that leave L2 in turn or last.
 __device__ __forceinline__ uint64_t once_policy() {
   uint64_t policy;
   asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
