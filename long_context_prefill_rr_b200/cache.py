@@ -146,6 +146,13 @@ def _used(stream, *tensors):
                 x.record_stream(stream)
 
 
+def _int32(name, *values):
+    """ctypes takes the low 32 bits of anything longer."""
+    for x in values:
+        if not -2 ** 31 <= x < 2 ** 31:
+            raise ValueError(f"{name} must fit 32 bits, got {x}")
+
+
 class RopeTable:
     """A rotation of the first ``rotary_dim`` of ``head_dim`` dimensions.
 
@@ -163,6 +170,8 @@ class RopeTable:
         if sections is not None and axis_of_pair is not None:
             raise ValueError("give sections or axis_of_pair, not both")
         rotary_dim = head_dim if rotary_dim is None else rotary_dim
+        _int32("head_dim", head_dim)
+        _int32("rotary_dim", rotary_dim)
         pairs = rotary_dim // 2
         freq = sec = ax = None
         if inv_freq is not None:
@@ -174,15 +183,19 @@ class RopeTable:
             axes = len(sections) if axes is None else axes
             if len(sections) != axes:
                 raise ValueError(f"sections must have {axes} values, got {len(sections)}")
-            sec = (_c.c_int32 * axes)(*[int(x) for x in sections])
+            values = [int(x) for x in sections]
+            _int32("sections", *values)
+            sec = (_c.c_int32 * axes)(*values)
         if axis_of_pair is not None:
             values = [int(x) for x in axis_of_pair]
             if len(values) != pairs:
                 raise ValueError(f"axis_of_pair must have {pairs} values, got {len(values)}")
-            axes = max(values) + 1 if axes is None else axes
+            _int32("axis_of_pair", *values)
+            axes = max(values, default=-1) + 1 if axes is None else axes
             ax = (_c.c_int32 * pairs)(*values)
         self.head_dim, self.rotary_dim, self.pairing = head_dim, rotary_dim, pairing
         self.axes = 1 if axes is None else axes
+        _int32("axes", self.axes)
         self.raw = _Rope()
         native._check(native.load().rra_rope_init(
             _c.byref(self.raw), head_dim, rotary_dim, self.axes, PAIRINGS[pairing], float(theta),
@@ -300,6 +313,7 @@ class PagedCache:
         if k.dim() != 4 or page_table.dim() != 2:
             raise ValueError("k must be [num_pages, heads_kv, page_size, head_dim] and page_table "
                              "[batch, max_pages]")
+        _int32("heads_q", heads_q)
         pages, hkv, ps, d = k.shape
         b, max_pages = page_table.shape
         _need(v, "v", device, k.dtype, k.shape)
