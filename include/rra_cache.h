@@ -22,7 +22,9 @@
  *     (e % page_size) * entry_stride, its value at the same place of v.
  *   - Softmax does not depend on the order of the entries: eviction changes it, and keys carry their
  *     position from the rotation. A tracked cache also holds, per entry and KV head, the attention
- *     weight accumulated so far and the token's ordinal, both [num_pages, heads_kv, page_size].
+ *     weight accumulated so far and the token's ordinal, both [num_pages, heads_kv, page_size]. Weights
+ *     come from rra_cache_decode alone, or from the caller: after a prompt that went through
+ *     rra_prefill and rra_cache_append they are all 0. len and seen are arrays of their own.
  *   - Lengths, page tables and ordinals live on the device and are read there: calls can be captured
  *     into a CUDA graph and replayed while they change.
  *   - A device-side mistake never reads or writes outside the cache; it sets the workspace's sticky
@@ -31,7 +33,9 @@
  *     outside [0, num_pages) as absent.
  *   - The calls that share a workspace must not overlap on the GPU, nor must the calls that write a
  *     cache and any other call on that cache. A workspace may serve several caches of the same sizes (the
- *     layers of a model); for other sizes it is laid out otherwise and has to be zero-filled again.
+ *     layers of a model); for other sizes it is laid out otherwise and has to be zero-filled again. That of
+ *     a tracked cache has room for the logits of a decode that adds weights, 4 bytes per sequence,
+ *     query head and entry of the page table's width.
  */
 #ifndef RRA_CACHE_H_
 #define RRA_CACHE_H_
@@ -155,7 +159,8 @@ rra_status rra_cache_decode(const rra_cache *cache, const rra_view *q, const rra
  * behind `budget` stay as they were. advance != 0 sets len[b] = budget; layers that share len
  * advance with the last one. Needs a tracked cache. Sequences that share a page, with another or with
  * themselves, or have a bad one are left as they are, since their entries could not move apart; this is
- * flagged if one of the sharing sequences is over the budget. */
+ * flagged if one of the sharing sequences is over the budget. The launch is sized by the page table's
+ * width, since lengths are on the device: a table much wider than its sequences costs time. */
 rra_status rra_cache_evict(const rra_cache *cache, int budget, int sinks, int recent, int advance,
                            rra_stream_t stream);
 

@@ -278,8 +278,9 @@ def rope(table, positions, q=None, k=None, v=None, *, q_out=None, k_out=None, v_
     """Rotates q and k [batch, heads, tokens, head_dim] (any strides, the last dimension
     contiguous) by int32 positions [axes, batch, tokens]; v, if given, is copied. Outputs default to
     new contiguous tensors, the layout of ``native.prefill``; ``q_out=q`` works in place.
-    ``inverse=True`` turns back: it takes the gradients of the outputs to those of the inputs.
-    Returns the outputs of the tensors that were given, in the order q, k, v."""
+    ``inverse=True`` turns back: it takes the gradients of the outputs to those of the inputs. (The call is
+    not recorded by autograd: in training call it from the forward and, with ``inverse=True``, from the
+    backward of a ``torch.autograd.Function``.) Returns the outputs of the tensors that were given, in the order q, k, v."""
     q_out = True if q is not None and q_out is None else q_out
     k_out = True if k is not None and k_out is None else k_out
     v_out = True if v is not None and v_out is None else v_out
@@ -303,8 +304,8 @@ class PagedCache:
 
     weight, order and seen come together; a cache that has them can be evicted from. The tensors'
     contents may change between calls, the tensors themselves stay (the object holds their
-    addresses). The object owns its workspace: its calls must not overlap on the GPU, and it has to
-    live until they are done on the GPU.
+    addresses); lengths and seen are tensors of their own. The object owns its workspace: its calls
+    must not overlap on the GPU, and it has to live until they are done on the GPU.
     """
 
     def __init__(self, k, v, page_table, lengths, *, heads_q, softmax_scale=-1.0, weight=None,
@@ -444,7 +445,9 @@ class PagedCache:
 
     def evict(self, budget, *, sinks=0, recent=0, advance=True, stream=None):
         """Cuts every sequence down to ``budget`` entries per KV head: the first ``sinks`` and last
-        ``recent`` tokens stay, then the entries of the largest accumulated weight."""
+        ``recent`` tokens stay, then the entries of the largest accumulated weight, the lower entry where
+        weights are equal. Weights are what ``decode(add_weight=True)`` has added, or the caller has written
+        to ``weight``: right after a prompt they are all 0. Sequences that share pages stay as they are."""
         if not self.tracked:
             raise ValueError("evict needs a cache with weight, order and seen")
         if not all(0 <= x < 2 ** 31 for x in (budget, sinks, recent)):
@@ -454,8 +457,8 @@ class PagedCache:
                       "rra_cache_evict")
 
     def check(self, stream=None):
-        """Synchronises and raises if a call met a bad page, length or shared page since the last
-        check (the error word is cleared)."""
+        """Synchronises ``stream`` (the current one by default) and raises if a call on it met a bad page,
+        length or shared page since the last check (the error word is cleared)."""
         word = _c.c_uint32(0)
         st = _call(self.device, self._lib.rra_check_device_status, self.ws.data_ptr(),
                    _raw_stream(stream, self.device), _c.byref(word))
