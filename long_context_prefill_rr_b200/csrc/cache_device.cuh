@@ -64,15 +64,13 @@ __device__ __forceinline__ uint4 ld_stream(const void *p) {
 
 // kRaise: decode multiplies the softmax weights, which are 1 at most, by 2^kRaise before it rounds them to
 // the element type. fp16 has a smallest step of 2^-24: raised by 15 (32768 is still below its largest
-// value) a weight keeps 2^-40 of the largest one. bf16 reaches as far as fp32, so that two of its largest
-// values add up to infinity: lowered by 31 as many as a sequence can have, 2^30, do not, and what is lost
-// are weights below 2^-95 of the largest and outputs' parts below 2^-118.
+// value) a weight keeps 2^-40 of the largest one. bf16 reaches as far as fp32.
 template <class T>
 struct Elem;
 
 template <>
 struct Elem<__nv_bfloat16> {
-  static constexpr int kRaise = -31;
+  static constexpr int kRaise = 0;
   static __device__ __forceinline__ float2 unpack(uint32_t u) {
     return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
   }

@@ -23,7 +23,6 @@
 // so the weights keep twice the bits of the element type at no cost: 2^-17 of themselves in bf16; in fp16
 // 2^-22 of themselves or 2^-40 of the largest weight, whichever is more, because they are raised by 2^15
 // first (unraised, entries 17.3 nats below an attention sink were 0 here and counted in the denominator).
-// bf16 weights are lowered by 2^31 in the same place: 2^30 of its largest values then add up without infinity.
 // With more than 8 heads to a KV head rows 8-15 hold 8 more of them, and the low parts take a second product.
 //
 // Measured on the way (128K entries, 32 / 8 heads of 128, 537 MB; the copy rate gives 82 us): fragments
@@ -86,13 +85,19 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
                : "memory");
   return v;
 }
+// What a mean is its weighted sum times: a sum of 0 (no weight at all) leaves 0, and NaN stays. (The hardware's
+// quotient, off by 2^-22 at most: the sums are well within its range. The exact one cost 0.3 us of a call of 7.)
+__device__ __forceinline__ float reciprocal_of_sum(float sum) {
+  return sum == 0.f ? 0.f : __fdividef(1.f, sum);
+}
+// A factor that joins means, 2^-126 at least (nothing beside the largest of them): an infinite or NaN mean
+// stays what it is.
+__device__ __forceinline__ float share_of(float f) { return fmaxf(f, FLT_MIN); }
+
 // Entry (of 8) behind column 2 t + e of an MMA tile. Columns may stand for the entries in any order, as
 // long as logits, weights and value rows agree; this one puts the rows that a read touches together
 // (columns 2 t, 2 t + 1 of the keys; the four values of t for the value rows) into different banks.
 __device__ __forceinline__ int entry_of(int t, int e) { return e ? 4 + ((t + 2) & 3) : t; }
-
-// 2^n for -126 < n < 127.
-constexpr float exp2_of(int n) { return n < 0 ? exp2_of(n + 1) * 0.5f : n > 0 ? exp2_of(n - 1) * 2.f : 1.f; }
 
 // Where a CTA's run of units starts.
 struct Cursor {
@@ -185,10 +190,11 @@ __device__ __forceinline__ void next_sequence(const CacheView &c, int items, Cur
   cur->units = units_of(cur->len);
 }
 
-// One query head's sums over a warp's entries of a piece, again: where values that are infinite or NaN meet
-// weights of 0 (logits of -inf) or the low parts of others, the matrix product has 0 * inf. Here an entry
-// without a weight is left out, and the other values that are not finite are noted for each dimension
-// apart from the sum. A lane takes D / 32 dimensions of eight entries at a time, for the heads and warps that
+// One query head's mean of a warp's entries of a piece, again: where values that are infinite or NaN meet
+// weights of 0 (logits of -inf) or the low parts of others, the matrix product has 0 * inf; and sums of bf16's
+// largest values pass fp32's range. Here an entry without a weight is left out, the other values that
+// are not finite are noted for each dimension apart from the sum, and the sum is kept 2^-31 as large (a
+// sequence has at most 2^30 entries). A lane takes D / 32 dimensions of eight entries at a time, for the heads and warps that
 // it happens to: 128K entries, 32 / 8 heads of 128, take 1.1 ms with an infinity under every KV head and 1.6 with
 // nothing but NaN, against 90 us. Code of its own, because the same within the loop below cost every call
 // 0.4 us, and 2 of 93 (32 sequences of up to 8K).
@@ -246,15 +252,17 @@ __device__ __noinline__ void add_up_again(const DecodeParams &p, int b, int kv_h
         for (int i = 0; i < PER; ++i) {
           const float y = v[n][i];
           const bool finite = fabsf(y) < INFINITY;
-          acc[i] = acc[i] * alpha + (finite ? w * exp2_of(Elem<T>::kRaise) * y : 0.f);
+          acc[i] = acc[i] * alpha + (finite ? w * 0x1p-31f * y : 0.f);
           if (!finite && !(y < 0.f)) plus |= 1u << i;
           if (!finite && !(y > 0.f)) minus |= 1u << i;
         }
       }
     }
   }
+  const float inv = reciprocal_of_sum(sum);
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
+    acc[i] *= inv * 0x1p31f;
     if ((plus >> i) & 1u) acc[i] += INFINITY;
     if ((minus >> i) & 1u) acc[i] -= INFINITY;
     out[lane * PER + i] = acc[i];
@@ -272,9 +280,9 @@ __global__ void __launch_bounds__(kThreads, decode_ctas(D))
   constexpr int S = kStages;
   constexpr uint32_t PITCH = kPitch<D>, STAGE = kStageBytes<D>;
   constexpr int ROW = D + 4;        // padded row of the merge buffer
-  // The weights in the registers, their sums and the outputs are 2^RAISE times too large. The sums lose the
-  // factor when they leave the registers, the outputs when they are divided by them.
-  constexpr float RAISE = Elem<T>::kRaise, LOWER = exp2_of(-Elem<T>::kRaise);
+  // Weights, their sums and the outputs are 2^RAISE times too large in the registers, where they are divided
+  // by one another.
+  constexpr int RAISE = Elem<T>::kRaise;
   static_assert(S <= 4 && S * STAGE >= TILE * ROW * 4, "exist masks, merge buffer");
   extern __shared__ __align__(128) uint8_t s_ring[];
   __shared__ int s_scan[20];
@@ -443,8 +451,9 @@ __global__ void __launch_bounds__(kThreads, decode_ctas(D))
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           // (the difference is rounded before the factor is added: it is never above 0)
-          const float w0 = fast_exp2(x[h][2 * i] - base + RAISE);
-          const float w1 = fast_exp2(x[h][2 * i + 1] - base + RAISE);
+          float y0 = x[h][2 * i] - base, y1 = x[h][2 * i + 1] - base;
+          if (RAISE) y0 += RAISE, y1 += RAISE;
+          const float w0 = fast_exp2(y0), w1 = fast_exp2(y1);
           l_run[h] += w0 + w1;
           hi[h][i] = Elem<T>::pack(w0, w1);
           const float2 f = Elem<T>::unpack(hi[h][i]);
@@ -479,25 +488,21 @@ __global__ void __launch_bounds__(kThreads, decode_ctas(D))
     copy_wait<0>();
     __syncwarp();
 
-    // heads with a sum that is not finite: sums and products with 0 tell
-    float not_finite[HT] = {};
-#pragma unroll
-    for (int i = 0; i < NH * 8; ++i)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) not_finite[q / 2 * (HT - 1)] += acc[i][q] * 0.f;
-
     // ---- the warps' results meet in shared memory
+    float inv_run[HT], not_finite[HT] = {};
 #pragma unroll
     for (int h = 0; h < HT; ++h) {
       l_run[h] += __shfl_xor_sync(0xffffffffu, l_run[h], 1);
       l_run[h] += __shfl_xor_sync(0xffffffffu, l_run[h], 2);
       if (t == 0) {
         s_m[warp][r + 8 * h] = m_run[h];
-        s_l[warp][r + 8 * h] = l_run[h] * LOWER;
+        s_l[warp][r + 8 * h] = l_run[h] / static_cast<float>(1 << RAISE);
       }
+      inv_run[h] = reciprocal_of_sum(l_run[h]);
     }
     // the thread's columns 2t and 2t + 1 of the permuted tiles are dimensions 16t .. 16t + 15 of
-    // each half; with one head per thread the products of the low parts are added here
+    // each half; with one head per thread the products of the low parts are added here. Products with 0 tell
+    // heads with a mean that is not finite.
 #pragma unroll
     for (int w = 0; w < HT; ++w)
 #pragma unroll
@@ -510,7 +515,8 @@ __global__ void __launch_bounds__(kThreads, decode_ctas(D))
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const float *o = acc[h * 8 + e + k];
-              y[k] = HT == 1 ? o[q] + o[q + 2] : o[q + 2 * w];
+              y[k] = (HT == 1 ? o[q] + o[q + 2] : o[q + 2 * w]) * inv_run[w];
+              not_finite[w] += y[k] * 0.f;
             }
             *reinterpret_cast<float4 *>(s_o(warp) + (r + 8 * w) * ROW + h * 64 + t * 16 + q * 8 + e) =
                 make_float4(y[0], y[1], y[2], y[3]);
@@ -540,23 +546,26 @@ __global__ void __launch_bounds__(kThreads, decode_ctas(D))
 #pragma unroll
       for (int w = 1; w < kWarps; ++w) mt = fmaxf(mt, s_m[w][row]);
       const float base = mt == -INFINITY ? 0.f : mt;
-      float l = 0.f;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      // factors of at least FLT_MIN (2^-126, nothing beside the largest one, 1) leave infinities as they are
+      float l = 0.f, part[kWarps];
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float f = exp2f(s_m[w][row] - base), g = fmaxf(f, FLT_MIN);
+        part[w] = exp2f(s_m[w][row] - base) * s_l[w][row];
+        l += part[w];
+      }
+      const float inv = reciprocal_of_sum(l);
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = share_of(part[w] * inv);
         const float4 x = *reinterpret_cast<const float4 *>(s_o(w) + row * ROW + col);
-        l += f * s_l[w][row];
-        o.x += g * x.x;
-        o.y += g * x.y;
-        o.z += g * x.z;
-        o.w += g * x.w;
+        o.x += f * x.x;
+        o.y += f * x.y;
+        o.z += f * x.z;
+        o.w += f * x.w;
       }
       if (whole) {
-        const float inv = l > 0.f ? LOWER / l : (l == 0.f ? 0.f : l);   // NaN stays
         *reinterpret_cast<uint2 *>(p.out + b * p.o_batch + (h0 + row) * p.o_head + col * 2) =
-            make_uint2(Elem<T>::pack(o.x * inv, o.y * inv), Elem<T>::pack(o.z * inv, o.w * inv));
+            make_uint2(Elem<T>::pack(o.x, o.y), Elem<T>::pack(o.z, o.w));
         if (col == 0) {
           const float l2 = base + log2f(l);
           p.lse2[b * c.hq + h0 + row] = l2;
@@ -581,26 +590,32 @@ __global__ void __launch_bounds__(kThreads, decode_ctas(D))
       if (s_scan[19]) {
         for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads) {
           const int row = i / (D / 4), col = (i - row * (D / 4)) * 4;
-          float mt = -INFINITY, l = 0.f;
-          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-          const float2 *ml = p.part_ml + (static_cast<int64_t>(item) + cta0) * TILE + row;
-          const float *po =
-              p.part_o + ((static_cast<int64_t>(item) + cta0) * TILE + row) * D + col;
-          for (int k = cta0; k <= cta1; ++k, ml += TILE, po += TILE * D) {
-            const float2 y = __ldcg(ml);
-            const float4 x = __ldcg(reinterpret_cast<const float4 *>(po));
-            const float mn = fmaxf(mt, y.x);
-            const float base = mn == -INFINITY ? 0.f : mn;
-            const float fa = exp2f(mt - base), fb = exp2f(y.x - base);
-            const float ga = fmaxf(fa, FLT_MIN), gb = fmaxf(fb, FLT_MIN);
-            mt = mn;
-            l = l * fa + y.y * fb;
-            o.x = o.x * ga + x.x * gb;
-            o.y = o.y * ga + x.y * gb;
-            o.z = o.z * ga + x.z * gb;
-            o.w = o.w * ga + x.w * gb;
+          float mt, l, lower = 1.f;
+          float4 o;
+          // sums past fp32's range are taken once more, 2^-31 as large
+          for (;; lower = 0x1p-31f) {
+            mt = -INFINITY, l = 0.f;
+            o = make_float4(0.f, 0.f, 0.f, 0.f);
+            const float2 *ml = p.part_ml + (static_cast<int64_t>(item) + cta0) * TILE + row;
+            const float *po =
+                p.part_o + ((static_cast<int64_t>(item) + cta0) * TILE + row) * D + col;
+            for (int k = cta0; k <= cta1; ++k, ml += TILE, po += TILE * D) {
+              const float2 y = __ldcg(ml);
+              const float4 x = __ldcg(reinterpret_cast<const float4 *>(po));
+              const float mn = fmaxf(mt, y.x);
+              const float base = mn == -INFINITY ? 0.f : mn;
+              const float fa = exp2f(mt - base), part = y.y * exp2f(y.x - base);
+              const float ga = share_of(fa), gb = share_of(part * lower);
+              mt = mn;
+              l = l * fa + part;
+              o.x = o.x * ga + x.x * gb;
+              o.y = o.y * ga + x.y * gb;
+              o.z = o.z * ga + x.z * gb;
+              o.w = o.w * ga + x.w * gb;
+            }
+            if (lower != 1.f || o.x * 0.f + o.y * 0.f + o.z * 0.f + o.w * 0.f == 0.f) break;
           }
-          const float inv = l > 0.f ? LOWER / l : (l == 0.f ? 0.f : l);
+          const float inv = reciprocal_of_sum(l * lower);
           *reinterpret_cast<uint2 *>(p.out + b * p.o_batch + (h0 + row) * p.o_head + col * 2) =
               make_uint2(Elem<T>::pack(o.x * inv, o.y * inv),
                          Elem<T>::pack(o.z * inv, o.w * inv));

@@ -67,9 +67,9 @@ def test_decode_long_tail_behind_a_sink(cuda_device, dtype, nats, group, d):
 @pytest.mark.parametrize("n", [3, 500, 20000])
 def test_decode_values_at_the_end_of_the_range(cuda_device, dtype, group, d, n):
     """The type's largest values, of one sign and of both: their sums pass fp32's range in bf16, their means
-    do not. All keys are 0, so all weights are equal (1 / n, exact but for the reciprocal of n, 2^-23);
-    each truncated addition is off by 2^-23 of the sum of the magnitudes, and a warp makes at most
-    n / 16 + 1 of them, the joins 300 more. What is past the largest value by less than half a step rounds
+    do not. All keys are 0, so all weights are equal; each truncated addition is off by 2^-23 of the sum of
+    the magnitudes, and a warp makes at most n / 16 + 1 of them, the joins, of 148 * 3 pieces at most but
+    fewer here, and the quotients by the sums of the weights (2^-22 each, three of them) 300 more. What is past the largest value by less than half a step rounds
     to it, and the mean of one value cannot be more."""
     hkv, ps, top = 2, 20, torch.finfo(dtype).max
     pages = -(-n // ps)
@@ -85,6 +85,34 @@ def test_decode_values_at_the_end_of_the_range(cuda_device, dtype, group, d, n):
     tol = half_step(dtype) * ref.abs() + top * ((n / 16 + 301) * 2.0 ** -23 + 2.0 ** -22)
     assert out.isfinite().all()
     assert ((out.double() - ref).abs() <= tol).all()
+    c.check()
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("group,d", [(1, 128), (12, 64)])
+@pytest.mark.parametrize("n", [3, 500, 20000])
+@pytest.mark.parametrize("size", ["smallest", "subnormal"])
+def test_decode_values_at_the_small_end_of_the_range(cuda_device, dtype, group, d, n, size):
+    """The type's smallest values, of one sign and of both. Products, sums and means have steps of 2^-149 in
+    fp32, which is 2^-23 of bf16's smallest normal value: n / 16 + 301 additions as above, for each head's
+    n products as much again in all. A subnormal output rounds to a step of the smallest subnormal."""
+    hkv, ps, low = 2, 20, torch.finfo(dtype).tiny * (1.0 if size == "smallest" else 0.25)
+    step = torch.finfo(dtype).tiny * torch.finfo(dtype).eps       # the smallest subnormal
+    pages = -(-n // ps)
+    k = torch.zeros(pages, hkv, ps, d, dtype=dtype, device="cuda")
+    v = torch.full((pages, hkv, ps, d), low, dtype=dtype, device="cuda")
+    v[..., 1::4] = -low
+    g = torch.Generator(device="cuda").manual_seed(n)
+    v[..., 2::4] *= torch.randint(0, 2, v[..., 2::4].shape, generator=g, device="cuda").to(dtype) * 2 - 1
+    assert float(v.double().abs().min()) == low
+    c = cache.PagedCache(k, v, ints([list(range(pages))]), ints([n]), heads_q=hkv * group)
+    out = c.decode(torch.ones(1, hkv * group, d, dtype=dtype, device="cuda"))
+    ref = v.transpose(0, 1).reshape(hkv, pages * ps, d)[:, :n].double().mean(1)
+    ref = ref.repeat_interleave(group, 0)[None]
+    tol = step / 2 + low * 2 * ((n / 16 + 301) * 2.0 ** -23 + 2.0 ** -22) * \
+        (4 if size == "subnormal" else 1)                         # the steps of 2^-149 are larger beside these
+    assert ((out.double() - ref).abs() <= tol).all(), float(((out.double() - ref).abs() / low).max())
+    assert out[..., 0].any()
     c.check()
 
 
